@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 __all__ = [
     "GqaError", "gqa_attn_fwd", "gqa_attn_fwd_ex", "gqa_attn_fwd_split", "gqa_attn_fwd_split_workspace_bytes",
@@ -26,6 +27,10 @@ __all__ = [
     "gqa_attn_decode_varlen_workspace_bytes", "gqa_attn_decode_varlen_num_splits",
     "gqa_attn_bwd", "gqa_attn_bwd_workspace_bytes", "attn_bwd", "gqa_attn_fwd_varlen_paged",
     "attn_fwd_varlen", "attn_decode_varlen",
+    "GqaRope", "GqaKv4Layout", "gqa_paged_plan", "gqa_qk_norm_rope", "gqa_qk_norm_rope_bwd",
+    "gqa_qk_norm_rope_bwd_workspace_bytes", "gqa_qk_norm_rope_append", "gqa_kv4_append", "gqa_kv4_gather",
+    "gqa_attn_decode_kv4", "gqa_attn_decode_kv4_workspace_bytes", "PagedPlan", "paged_plan", "qk_norm_rope",
+    "qk_norm_rope_bwd", "qk_norm_rope_append", "kv4_pool", "kv4_append", "kv4_gather", "attn_decode_kv4",
     "GQA_OK", "GQA_ERR_INVALID_ARGUMENT", "GQA_ERR_UNSUPPORTED", "GQA_ERR_WORKSPACE",
     "GQA_ERR_CUDA", "GQA_ERR_TIMEOUT",
 ]
@@ -106,6 +111,39 @@ _lib.gqa_attn_bwd_workspace_bytes.restype = _sz
 _lib.gqa_attn_bwd_workspace_bytes.argtypes = [_i32] * 6
 _lib.gqa_attn_bwd.restype = _i32
 _lib.gqa_attn_bwd.argtypes = [_vp] * 9 + [_i32] * 6 + [_ll] * 4 + [_f32, _i32, _vp, _sz, _vp]
+
+
+class GqaRope(ctypes.Structure):
+    """C ``gqa_rope``: norm weights, angle tables and positions (device addresses; 0 = none)."""
+    _fields_ = [("q_weight", _vp), ("k_weight", _vp), ("cos", _vp), ("sin", _vp), ("positions", _vp),
+                ("positions_sb", _ll), ("n_positions", _i32), ("rot", _i32), ("interleaved", _i32),
+                ("weight_fp32", _i32), ("eps", _f32)]
+
+
+class GqaKv4Layout(ctypes.Structure):
+    """C ``gqa_kv4_layout``: byte strides (page, head) of a 4-bit pool."""
+    _fields_ = [("sb", _ll), ("sh", _ll)]
+
+
+_rope, _lay4 = ctypes.POINTER(GqaRope), ctypes.POINTER(GqaKv4Layout)
+_lib.gqa_paged_plan.restype = _i32
+_lib.gqa_paged_plan.argtypes = [_vp] * 11 + [_i32] * 6 + [_vp]
+_lib.gqa_qk_norm_rope.restype = _i32
+_lib.gqa_qk_norm_rope.argtypes = [_vp] * 4 + [_i32] * 5 + [_lay] * 4 + [_rope, _vp]
+_lib.gqa_qk_norm_rope_append.restype = _i32
+_lib.gqa_qk_norm_rope_append.argtypes = [_vp] * 7 + [_i32] * 6 + [_lay] * 6 + [_rope, _vp]
+_lib.gqa_qk_norm_rope_bwd_workspace_bytes.restype = _sz
+_lib.gqa_qk_norm_rope_bwd_workspace_bytes.argtypes = [_i32] * 5
+_lib.gqa_qk_norm_rope_bwd.restype = _i32
+_lib.gqa_qk_norm_rope_bwd.argtypes = [_vp] * 8 + [_i32] * 5 + [_lay] * 6 + [_rope, _vp, _sz, _vp]
+_lib.gqa_kv4_append.restype = _i32
+_lib.gqa_kv4_append.argtypes = [_vp] * 5 + [_i32] * 5 + [_lay] * 2 + [_lay4] * 2 + [_vp]
+_lib.gqa_kv4_gather.restype = _i32
+_lib.gqa_kv4_gather.argtypes = [_vp] * 5 + [_i32] * 5 + [_lay4] * 2 + [_lay] * 2 + [_vp]
+_lib.gqa_attn_decode_kv4_workspace_bytes.restype = _sz
+_lib.gqa_attn_decode_kv4_workspace_bytes.argtypes = [_i32] * 7
+_lib.gqa_attn_decode_kv4.restype = _i32
+_lib.gqa_attn_decode_kv4.argtypes = [_vp] * 6 + [_i32] * 9 + [_lay4] * 2 + [_f32, _i32, _vp, _sz, _vp]
 _lib.gqa_status_string.restype = ctypes.c_char_p
 _lib.gqa_status_string.argtypes = [_i32]
 _lib.gqa_get_device_error.restype = _i32
@@ -269,6 +307,76 @@ def gqa_attn_bwd(q, k, v, o, dout, lse, dq, dk, dv, B, Hq, Hkv, Tq, Tk, D, k_sb,
     """C ``gqa_attn_bwd``: dq, dk, dv of the causal GQA forward for the output gradient dout."""
     return _lib.gqa_attn_bwd(q, k, v, o, dout, lse, dq, dk, dv, B, Hq, Hkv, Tq, Tk, D, k_sb, k_sh, v_sb, v_sh,
                              float(softmax_scale), int(window), workspace, workspace_bytes, stream)
+
+
+def gqa_paged_plan(seqlens, keep, new_tokens, block_table, free_list, free_count, seqlens_out, cu_seqlens, positions,
+                   slots, free_count_out, S, max_pages, page_size, num_pages, free_capacity, max_tokens,
+                   stream=None) -> int:
+    """C ``gqa_paged_plan``; pointers are integers (device addresses). Returns the status."""
+    return _lib.gqa_paged_plan(seqlens, keep, new_tokens, block_table, free_list, free_count, seqlens_out, cu_seqlens,
+                               positions, slots, free_count_out, S, max_pages, page_size, num_pages, free_capacity,
+                               max_tokens, stream)
+
+
+def gqa_qk_norm_rope(q, k, q_out, k_out, B, T, Hq, Hkv, D, q_layout, k_layout, q_out_layout, k_out_layout, rope,
+                     stream=None) -> int:
+    """C ``gqa_qk_norm_rope``; ``rope`` is a GqaRope, layouts GqaLayout or (sb, sh, st) tuples."""
+    return _lib.gqa_qk_norm_rope(q, k, q_out, k_out, B, T, Hq, Hkv, D, _layout(q_layout), _layout(k_layout),
+                                 _layout(q_out_layout), _layout(k_out_layout), rope, stream)
+
+
+def gqa_qk_norm_rope_append(q, k, v, q_out, k_pool, v_pool, slots, N, Hq, Hkv, D, page_size, num_pages, q_layout,
+                            k_layout, v_layout, q_out_layout, k_pool_layout, v_pool_layout, rope, stream=None) -> int:
+    """C ``gqa_qk_norm_rope_append``: the norm and rotation, with k and v written into their pages."""
+    return _lib.gqa_qk_norm_rope_append(q, k, v, q_out, k_pool, v_pool, slots, N, Hq, Hkv, D, page_size, num_pages,
+                                        _layout(q_layout), _layout(k_layout), _layout(v_layout),
+                                        _layout(q_out_layout), _layout(k_pool_layout), _layout(v_pool_layout), rope,
+                                        stream)
+
+
+def gqa_qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hkv, D) -> int:
+    return int(_lib.gqa_qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hkv, D))
+
+
+def gqa_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, dq_weight, dk_weight, B, T, Hq, Hkv, D, dq_out_layout,
+                         dk_out_layout, q_layout, k_layout, dq_layout, dk_layout, rope, workspace=None,
+                         workspace_bytes=0, stream=None) -> int:
+    """C ``gqa_qk_norm_rope_bwd``: gradients of q, k and the norm weights."""
+    return _lib.gqa_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, dq_weight, dk_weight, B, T, Hq, Hkv, D,
+                                     _layout(dq_out_layout), _layout(dk_out_layout), _layout(q_layout),
+                                     _layout(k_layout), _layout(dq_layout), _layout(dk_layout), rope, workspace,
+                                     workspace_bytes, stream)
+
+
+def _layout4(x):
+    return x if isinstance(x, GqaKv4Layout) else GqaKv4Layout(*x)
+
+
+def gqa_kv4_append(k, v, k_pool, v_pool, slots, N, Hkv, D, page_size, num_pages, k_layout, v_layout, k_pool_layout,
+                   v_pool_layout, stream=None) -> int:
+    """C ``gqa_kv4_append``; pool layouts are GqaKv4Layout or (sb, sh) tuples in bytes."""
+    return _lib.gqa_kv4_append(k, v, k_pool, v_pool, slots, N, Hkv, D, page_size, num_pages, _layout(k_layout),
+                               _layout(v_layout), _layout4(k_pool_layout), _layout4(v_pool_layout), stream)
+
+
+def gqa_kv4_gather(k_pool, v_pool, k, v, slots, N, Hkv, D, page_size, num_pages, k_pool_layout, v_pool_layout,
+                   k_layout, v_layout, stream=None) -> int:
+    """C ``gqa_kv4_gather``: rows of the 4-bit cache back as bf16."""
+    return _lib.gqa_kv4_gather(k_pool, v_pool, k, v, slots, N, Hkv, D, page_size, num_pages, _layout4(k_pool_layout),
+                               _layout4(v_pool_layout), _layout(k_layout), _layout(v_layout), stream)
+
+
+def gqa_attn_decode_kv4_workspace_bytes(B, Hq, Hkv, Tq, max_seqlen_k, D, window=0) -> int:
+    return int(_lib.gqa_attn_decode_kv4_workspace_bytes(B, Hq, Hkv, Tq, max_seqlen_k, D, window))
+
+
+def gqa_attn_decode_kv4(q, k_pool, v_pool, o, seqlens_k, block_table, page_size, num_pages, max_pages, B, Hq, Hkv, Tq,
+                        max_seqlen_k, D, k_layout, v_layout, softmax_scale=0.0, window=0, workspace=None,
+                        workspace_bytes=0, stream=None) -> int:
+    """C ``gqa_attn_decode_kv4``: decode over a paged cache held in 4 bits."""
+    return _lib.gqa_attn_decode_kv4(q, k_pool, v_pool, o, seqlens_k, block_table, page_size, num_pages, max_pages, B,
+                                    Hq, Hkv, Tq, max_seqlen_k, D, _layout4(k_layout), _layout4(v_layout),
+                                    softmax_scale, window, workspace, workspace_bytes, stream)
 
 
 def gqa_status_string(status: int) -> str:
@@ -665,3 +773,372 @@ def _attn_fwd_varlen_paged(q, k_pool, v_pool, cu_seqlens_q, seqlens_q, seqlens_k
     if st != GQA_OK:
         raise GqaError(st, "gqa_attn_fwd_varlen_paged")
     return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------- around the attention calls
+def _on_device(**tensors):
+    """The CUDA device that all given tensors (None: left out) are on; it must be the current one."""
+    torch = _torch()
+    device = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if device is None:
+            device = t.device
+            if device.type != "cuda":
+                raise TypeError(f"{name} must be a CUDA tensor")
+        elif t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the first operand on {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the operands are on {device}, which is not the current device")
+    return device
+
+
+def _keep_until(stream, *tensors):
+    """Tensors allocated here for a call on another stream than the current one stay allocated
+    until that stream has passed the call."""
+    if stream is None:
+        return
+    torch = _torch()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
+def _int32(t, name, shape=None):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t
+
+
+def _bf16_rows(t, name, shape=None, dims=4):
+    """Layout (sb, sh, st) of a bf16 operand [B, H, T, D], or [T, H, D] when dims is 3."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bf16 tensor")
+    if t.dim() != dims or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape) if shape else f'of {dims} axes'}, not {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name}: the last (D) axis must be contiguous")
+    return (st[0], st[1], st[2]) if dims == 4 else (0, st[1], st[0])
+
+
+class PagedPlan(NamedTuple):
+    """What ``paged_plan`` returns: int32 CUDA tensors."""
+    seqlens_k: object   # [S] rows each request holds afterwards
+    cu_seqlens: object  # [S + 1] first token of each request
+    positions: object   # [max_tokens]
+    slots: object       # [max_tokens] cache rows, -1: none
+    free_count: object  # [1]
+
+
+def paged_plan(seqlens, new_tokens, block_table, free_list, free_count, *, page_size, num_pages, max_tokens, keep=None,
+               out=None, stream=None):
+    """The plan of one step over a paged cache, made on the device from request lengths.
+
+    Request s holds ``seqlens[s]`` rows, keeps the first ``keep[s]`` (default: all; 0 for a
+    finished request) and adds ``new_tokens[s]``. Pages given back are pushed on the stack
+    ``free_list[:free_count]`` in (request, page) order, then the wanted ones are popped;
+    ``block_table`` [S, max_pages] and ``free_list`` are updated in place. Returns a PagedPlan:
+    new lengths (``seqlens_k`` of the attention calls), token boundaries (``cu_seqlens_q``),
+    ``positions`` and ``slots`` of ``max_tokens`` tokens (padding: 0 and -1), and the new free
+    count. ``out`` is a PagedPlan to write into; its ``seqlens_k`` and ``free_count`` may be
+    ``seqlens`` and ``free_count`` themselves. Lengths that do not fit, or too few pages, leave
+    everything as it is and are reported by ``gqa_get_device_error``.
+    """
+    S = seqlens.numel()
+    for t, n in ((seqlens, "seqlens"), (new_tokens, "new_tokens")):
+        _int32(t, n, (S,))
+    if keep is not None:
+        _int32(keep, "keep", (S,))
+    _int32(block_table, "block_table")
+    _int32(free_list, "free_list")
+    if block_table.dim() != 2 or block_table.shape[0] != S or free_list.dim() != 1:
+        raise ValueError("block_table must be [S, max_pages] and free_list [capacity]")
+    if _int32(free_count, "free_count").numel() != 1:
+        raise ValueError("free_count must hold one value")
+    device = _on_device(seqlens=seqlens, new_tokens=new_tokens, block_table=block_table, free_list=free_list,
+                        free_count=free_count, keep=keep)
+    max_tokens = int(max_tokens)
+    fresh = None
+    if out is None:
+        if max_tokens <= 0:
+            raise ValueError("max_tokens must be positive")
+        pad = -max_tokens % 4  # positions and slots start on 16 bytes
+        fresh = seqlens.new_empty(2 * (max_tokens + pad) + 2 * S + 2)
+        pos, _, slots, _, cu, lens, count = fresh.split([max_tokens, pad, max_tokens, pad, S + 1, S, 1])
+        out = PagedPlan(lens, cu, pos, slots, count)
+    else:
+        for t, n, shape in zip(out, PagedPlan._fields, ((S,), (S + 1,), (max_tokens,), (max_tokens,), (1,))):
+            _int32(t, n, shape)
+        _on_device(seqlens=seqlens, **out._asdict())
+    st = _lib.gqa_paged_plan(seqlens.data_ptr(), _ptr(keep), new_tokens.data_ptr(), block_table.data_ptr(),
+                             free_list.data_ptr(), free_count.data_ptr(), out.seqlens_k.data_ptr(),
+                             out.cu_seqlens.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
+                             out.free_count.data_ptr(), S, block_table.shape[1], page_size, num_pages,
+                             free_list.numel(), max_tokens, _stream_handle(stream))
+    if st != GQA_OK:
+        raise GqaError(st, "gqa_paged_plan")
+    _keep_until(stream, fresh)
+    return out
+
+
+def _rope_args(D, B, T, q_weight, k_weight, eps, cos, sin, positions, interleaved):
+    """(GqaRope, operands by name)."""
+    torch = _torch()
+    r = GqaRope(eps=eps, interleaved=bool(interleaved))
+    kinds = set()
+    for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        if w.dtype not in (torch.bfloat16, torch.float32) or w.shape != (D,) or not w.is_contiguous():
+            raise TypeError(f"{n} must be a contiguous bf16 or fp32 tensor [{D}]")
+        kinds.add(w.dtype)
+        setattr(r, n, w.data_ptr())
+    if len(kinds) > 1:
+        raise TypeError("q_weight and k_weight must have the same type")
+    r.weight_fp32 = torch.float32 in kinds
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    if cos is None:
+        if positions is not None:
+            raise ValueError("positions need cos and sin")
+    else:
+        for n, t in (("cos", cos), ("sin", sin)):
+            if t.dtype != torch.float32 or t.dim() != 2 or t.shape != cos.shape or not t.is_contiguous():
+                raise TypeError(f"{n} must be a contiguous fp32 tensor [positions, rot / 2]")
+        r.cos, r.sin, r.n_positions, r.rot = cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1]
+        if positions is not None:
+            _int32(positions, "positions")
+            if positions.shape != (T,) and positions.shape != (B, T):
+                raise ValueError(f"positions must be [{T}] or [{B}, {T}]")
+            r.positions, r.positions_sb = positions.data_ptr(), T if positions.dim() == 2 else 0
+    return r, {"q_weight": q_weight, "k_weight": k_weight, "cos": cos, "sin": sin, "positions": positions}
+
+
+def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, eps=1e-6, cos=None, sin=None, positions=None,
+                 interleaved=False, q_out=None, k_out=None, stream=None):
+    """RMS norm of each query and key head, then the position rotation, in one pass.
+
+    q [B, Hq, T, D] and k [B, Hkv, T, D], bf16, any batch/head/row strides (so the projection's
+    [B, T, heads, D] output is read where it lies). ``q_weight``/``k_weight`` [D] (bf16 or fp32;
+    None: that side is not normalised); ``cos``/``sin`` fp32 [positions, rot / 2] (None: no
+    rotation; rot = D rotates whole rows); ``positions`` int32 [T] or [B, T] (default 0 .. T - 1);
+    pairs are (i, i + rot/2), or (2i, 2i + 1) when ``interleaved``. Returns contiguous (q, k) of
+    the same shapes, or writes ``q_out``/``k_out`` (which may be q and k themselves).
+    """
+    lq = _bf16_rows(q, "q")
+    B, Hq, T, D = q.shape
+    lk = _bf16_rows(k, "k")
+    Hkv = k.shape[1]
+    if k.shape != (B, Hkv, T, D):
+        raise ValueError("q and k must be [B, Hq, T, D] and [B, Hkv, T, D]")
+    r, more = _rope_args(D, B, T, q_weight, k_weight, eps, cos, sin, positions, interleaved)
+    _on_device(q=q, k=k, q_out=q_out, k_out=k_out, **more)
+    fresh_q = fresh_k = None
+    if q_out is None:
+        q_out = fresh_q = q.new_empty(q.shape)
+    if k_out is None:
+        k_out = fresh_k = k.new_empty(k.shape)
+    st = gqa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), B, T, Hq, Hkv, D, lq, lk,
+                          _bf16_rows(q_out, "q_out", q.shape), _bf16_rows(k_out, "k_out", k.shape), r,
+                          _stream_handle(stream))
+    if st != GQA_OK:
+        raise GqaError(st, "gqa_qk_norm_rope")
+    _keep_until(stream, fresh_q, fresh_k)
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, *, q_weight=None, k_weight=None, eps=1e-6, cos=None, sin=None,
+                     positions=None, interleaved=False, dq=None, dk=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dq_weight, dk_weight) of ``qk_norm_rope(q, k, ...)`` for the gradients of
+    its outputs (for instance ``attn_bwd``'s dq and dk). The weights' gradients are fp32 [D], None
+    for a side without a weight. dq and dk may be dq_out and dk_out themselves."""
+    torch = _torch()
+    lq = _bf16_rows(q, "q")
+    B, Hq, T, D = q.shape
+    lk = _bf16_rows(k, "k")
+    Hkv = k.shape[1]
+    if k.shape != (B, Hkv, T, D):
+        raise ValueError("q and k must be [B, Hq, T, D] and [B, Hkv, T, D]")
+    r, more = _rope_args(D, B, T, q_weight, k_weight, eps, cos, sin, positions, interleaved)
+    device = _on_device(dq_out=dq_out, dk_out=dk_out, q=q, k=k, dq=dq, dk=dk, workspace=workspace, **more)
+    fresh = []
+    if dq is None:
+        fresh.append(dq := q.new_empty(q.shape))
+    if dk is None:
+        fresh.append(dk := k.new_empty(k.shape))
+    dqw = torch.empty(D, dtype=torch.float32, device=device) if q_weight is not None else None
+    dkw = torch.empty(D, dtype=torch.float32, device=device) if k_weight is not None else None
+    fresh += [dqw, dkw]
+    if workspace is None and (dqw is not None or dkw is not None):
+        workspace = torch.empty(max(1, gqa_qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hkv, D)), dtype=torch.uint8,
+                                device=device)
+        fresh.append(workspace)
+    st = gqa_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
+                              dk.data_ptr(), _ptr(dqw), _ptr(dkw), B, T, Hq, Hkv, D,
+                              _bf16_rows(dq_out, "dq_out", q.shape), _bf16_rows(dk_out, "dk_out", k.shape), lq, lk,
+                              _bf16_rows(dq, "dq", q.shape), _bf16_rows(dk, "dk", k.shape), r, _ptr(workspace),
+                              workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                              _stream_handle(stream))
+    if st != GQA_OK:
+        raise GqaError(st, "gqa_qk_norm_rope_bwd")
+    _keep_until(stream, *fresh)
+    return dq, dk, dqw, dkw
+
+
+def qk_norm_rope_append(q, k, v, k_pool, v_pool, slots, *, q_weight=None, k_weight=None, eps=1e-6, cos=None, sin=None,
+                        positions=None, interleaved=False, pool_layout="NHD", q_out=None, stream=None):
+    """``qk_norm_rope`` for N packed tokens that writes the keys and values into their cache pages.
+
+    q [N, Hq, D], k and v [N, Hkv, D], any token/head strides; ``slots`` int32 [N] (``paged_plan``'s;
+    distinct, negative: no row is written); ``positions`` int32 [N]. k_pool and v_pool are the bf16
+    pools of ``attn_decode_varlen``, [pages, page, Hkv, D] ("NHD") or [pages, Hkv, page, D] ("HND").
+    Returns the queries [N, Hq, D].
+    """
+    lq = _bf16_rows(q, "q", dims=3)
+    N, Hq, D = q.shape
+    lk = _bf16_rows(k, "k", dims=3)
+    Hkv = k.shape[1]
+    lv = _bf16_rows(v, "v", (N, Hkv, D), dims=3)
+    if k.shape != (N, Hkv, D):
+        raise ValueError("q and k must be [N, Hq, D] and [N, Hkv, D]")
+    _int32(slots, "slots", (N,))
+    sk = _bf16_rows(k_pool, "k_pool")
+    sv = _bf16_rows(v_pool, "v_pool", k_pool.shape)
+    if pool_layout == "NHD":
+        pages, page, heads, _ = k_pool.shape
+        sk, sv = (sk[0], sk[2], sk[1]), (sv[0], sv[2], sv[1])
+    elif pool_layout == "HND":
+        pages, heads, page, _ = k_pool.shape
+    else:
+        raise ValueError("pool_layout must be 'NHD' or 'HND'")
+    if heads != Hkv or k_pool.shape[3] != D:
+        raise ValueError("the pools' heads and rows must be k's")
+    r, more = _rope_args(D, 1, N, q_weight, k_weight, eps, cos, sin, positions, interleaved)
+    _on_device(q=q, k=k, v=v, k_pool=k_pool, v_pool=v_pool, slots=slots, q_out=q_out, **more)
+    fresh = None
+    if q_out is None:
+        q_out = fresh = q.new_empty(q.shape)
+    st = gqa_qk_norm_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_pool.data_ptr(),
+                                 v_pool.data_ptr(), slots.data_ptr(), N, Hq, Hkv, D, page, pages, lq, lk, lv,
+                                 _bf16_rows(q_out, "q_out", q.shape, dims=3), sk, sv, r, _stream_handle(stream))
+    if st != GQA_OK:
+        raise GqaError(st, "gqa_qk_norm_rope_append")
+    _keep_until(stream, fresh)
+    return q_out
+
+
+def kv4_pool(num_pages, num_heads, page_size, D, device=None):
+    """A pool of zero rows for a paged cache held in 4 bits: uint8 [pages, Hkv, page, D / 2 + 4]."""
+    torch = _torch()
+    return torch.zeros((num_pages, num_heads, page_size, D // 2 + 4), dtype=torch.uint8,
+                       device=torch.cuda.current_device() if device is None else device)
+
+
+def _kv4_layout(t, name, D, shape=None):
+    """Byte strides (page, head) of a 4-bit pool [pages, Hkv, page, D / 2 + 4]."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
+        raise TypeError(f"{name} must be a uint8 tensor")
+    if t.dim() != 4 or t.shape[3] != D // 2 + 4 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be [pages, Hkv, page, {D // 2 + 4}] (both pools alike), not {tuple(t.shape)}")
+    st = t.stride()
+    if st[3] != 1 or st[2] != t.shape[3]:
+        raise ValueError(f"{name}: the rows of a page must be packed")
+    return st[0], st[1]
+
+
+def kv4_append(k, v, k_pool, v_pool, slots, *, stream=None):
+    """Write k and v, bf16 [N, Hkv, D] (any token/head strides), as 4-bit rows to the rows
+    ``slots`` (int32 [N], distinct; negative: none) of the pools [pages, Hkv, page, D / 2 + 4]."""
+    lk = _bf16_rows(k, "k", dims=3)
+    N, Hkv, D = k.shape
+    lv = _bf16_rows(v, "v", k.shape, dims=3)
+    _int32(slots, "slots", (N,))
+    sk = _kv4_layout(k_pool, "k_pool", D)
+    sv = _kv4_layout(v_pool, "v_pool", D, k_pool.shape)
+    if k_pool.shape[1] != Hkv:
+        raise ValueError("the pools' heads must be k's")
+    _on_device(k=k, v=v, k_pool=k_pool, v_pool=v_pool, slots=slots)
+    st = gqa_kv4_append(k.data_ptr(), v.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), slots.data_ptr(), N, Hkv, D,
+                        k_pool.shape[2], k_pool.shape[0], lk, lv, sk, sv, _stream_handle(stream))
+    if st != GQA_OK:
+        raise GqaError(st, "gqa_kv4_append")
+
+
+def kv4_gather(k_pool, v_pool, slots, *, k=None, v=None, stream=None):
+    """Rows ``slots`` (int32 [N]) of the 4-bit pools as bf16 (k, v) [N, Hkv, D]; a slot outside
+    the pool gives zeros."""
+    torch = _torch()
+    if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
+        raise TypeError("k_pool must be a uint8 tensor [pages, Hkv, page, D / 2 + 4]")
+    pages, Hkv, page, row = k_pool.shape
+    D = 2 * (row - 4)
+    sk = _kv4_layout(k_pool, "k_pool", D)
+    sv = _kv4_layout(v_pool, "v_pool", D, k_pool.shape)
+    N = _int32(slots, "slots").numel()
+    _on_device(k_pool=k_pool, v_pool=v_pool, slots=slots, k=k, v=v)
+    fresh_k = fresh_v = None
+    if k is None:
+        k = fresh_k = torch.empty((N, Hkv, D), dtype=torch.bfloat16, device=k_pool.device)
+    if v is None:
+        v = fresh_v = torch.empty((N, Hkv, D), dtype=torch.bfloat16, device=k_pool.device)
+    st = gqa_kv4_gather(k_pool.data_ptr(), v_pool.data_ptr(), k.data_ptr(), v.data_ptr(), slots.data_ptr(), N, Hkv, D,
+                        page, pages, sk, sv, _bf16_rows(k, "k", (N, Hkv, D), dims=3),
+                        _bf16_rows(v, "v", (N, Hkv, D), dims=3), _stream_handle(stream))
+    if st != GQA_OK:
+        raise GqaError(st, "gqa_kv4_gather")
+    _keep_until(stream, fresh_k, fresh_v)
+    return k, v
+
+
+def attn_decode_kv4(q, k_pool, v_pool, seqlens_k, block_table, *, max_seqlen_k=None, scale=None, window=0, out=None,
+                    workspace=None, stream=None):
+    """``attn_decode_varlen`` over a paged cache held in 4 bits (``kv4_append``'s pools).
+
+    q [B, Hq, Tq, D] (Tq <= 16; or [B, Hq, D]); sequence b's queries are the last Tq of its
+    ``seqlens_k[b]`` positions, a query at a negative position gets zeros; ``block_table`` int32
+    [B, max_pages]. ``workspace``: a uint8 CUDA tensor of gqa_attn_decode_kv4_workspace_bytes(...)
+    bytes, allocated here when omitted.
+    """
+    torch = _torch()
+    if not isinstance(q, torch.Tensor) or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.dim() not in (3, 4):
+        raise TypeError("q must be a contiguous bf16 tensor [B, Hq, Tq, D] or [B, Hq, D]")
+    B, Hq, D = q.shape[0], q.shape[1], q.shape[-1]
+    Tq = q.shape[2] if q.dim() == 4 else 1
+    sk = _kv4_layout(k_pool, "k_pool", D)
+    sv = _kv4_layout(v_pool, "v_pool", D, k_pool.shape)
+    pages, Hkv, page, _ = k_pool.shape
+    _int32(seqlens_k, "seqlens_k", (B,))
+    _int32(block_table, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    max_pages = block_table.shape[1]
+    max_seqlen_k = max_pages * page if max_seqlen_k is None else int(max_seqlen_k)
+    _on_device(q=q, k_pool=k_pool, v_pool=v_pool, seqlens_k=seqlens_k, block_table=block_table, out=out,
+               workspace=workspace)
+    fresh_out = fresh_ws = None
+    if out is None:
+        out = fresh_out = q.new_empty(q.shape)
+    elif out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 tensor shaped like q")
+    if workspace is None:
+        need = gqa_attn_decode_kv4_workspace_bytes(B, Hq, Hkv, Tq, max_seqlen_k, D, window)
+        if need:
+            workspace = fresh_ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    st = gqa_attn_decode_kv4(q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), out.data_ptr(), seqlens_k.data_ptr(),
+                             block_table.data_ptr(), page, pages, max_pages, B, Hq, Hkv, Tq, max_seqlen_k, D, sk, sv,
+                             float(scale or 0.0), window, _ptr(workspace),
+                             workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                             _stream_handle(stream))
+    if st != GQA_OK:
+        raise GqaError(st, "gqa_attn_decode_kv4")
+    _keep_until(stream, fresh_out, fresh_ws)
+    return out

@@ -1,0 +1,586 @@
+// Decode over a paged cache held in 4 bits (rows as kv4_rows_sm100.cuh writes them): up to 16
+// new queries a sequence, any group size, optional sliding window.
+//
+// A stored row is k_j = s_j c_j + m_j with codes c in 0..15, so with the 16 added to every code
+// by the bit pattern below
+//   q . k_j = s_j (q . (16 + c_j) - 16 sum(q)) + m_j sum(q),
+//   sum_j p_j v_j = sum_j w_j (16 + c_j) - 24 sum_j w_j + sum_j p_j (m_j + 8 s_j),  w_j = bf16(p_j s_j).
+// A code becomes a bf16 number with one shift and one logic operation for two of them (16 + c is
+// the bits 0x4180 | c << 3, exact), the scales stay out of the products, and the products run on
+// tensor cores in bf16 with fp32 sums. w is the only rounding besides the output's: it is taken
+// about the middle of the code range (8), so it costs what rounding P to bf16 costs. A row's NaN
+// can only reach the queries that see the key: the codes themselves are always finite.
+//
+// Keys are the M dimension of the products and query rows their N (8 a tile), so that one
+// unpacked fragment serves every query row of the KV head. mma m16n8k16 takes any order of the
+// contracted index as long as both operands agree; the orders here are chosen so that every
+// fragment is whole 32-bit words of the packed rows: a row is D/8 + 1 words, which makes the
+// lanes' words (keys 4g + c, words t + 4i for K; keys 8t + c, words g + 8i for V) fall on 32
+// different banks without padding or swizzle. P goes from its accumulator layout to the B
+// operand's with one 8x8 transpose a tile.
+//
+// Work: the tiles of 32 keys of every (sequence, KV head, row chunk) laid end to end are cut
+// into equal runs, one per CTA, so all CTAs finish together whatever the lengths. In a CTA the
+// warps take tiles in turn, each with a ring of its own that its own lanes fill with bulk
+// copies (a page's rows of one head are contiguous): no warp waits for another until the
+// piece ends. A unit cut between CTAs leaves fp32 partials that a second kernel merges in
+// a fixed order. Bound by HBM: D + 8 bytes a key and KV head.
+#pragma once
+
+#include "sm100_ptx.cuh"
+
+namespace gqa {
+
+constexpr int kD4Warps = 8;
+constexpr int kD4Threads = 32 * kD4Warps;
+constexpr int kD4Keys = 32;  // keys a tile
+
+struct Dec4Params {
+    const __nv_bfloat16* q;  // [B, Hq, Tq, D]
+    __nv_bfloat16* o;
+    const uint8_t* k;
+    const uint8_t* v;
+    long long k_sb, k_sh, v_sb, v_sh;  // bytes
+    const int* seqlens;
+    const int* table;
+    int B, Hq, Hkv, G, Tq;
+    int n_rc;  // chunks of query rows a group
+    int page_size, num_pages, max_pages, capacity, window;
+    float scale_log2;
+    float* part;      // [2 * gridDim.x, rows, D] partial outputs
+    float* part_lse;  // [2 * gridDim.x, rows] log2-domain log-sum-exp
+    uint32_t* err;
+    unsigned long long timeout_ns;
+};
+
+template <int D, int NT>
+struct Dec4Cfg {
+    static constexpr int kRows = 8 * NT;            // query rows a CTA takes
+    static constexpr int kRow = D / 2 + 4;          // bytes of a stored row
+    static constexpr int kTile = kD4Keys * kRow;    // K or V rows of a tile
+    static constexpr int kStage = 2 * kTile;
+    static constexpr int kStages = NT == 4 ? 4 : 3;
+    static constexpr int kCtasPerSm = NT == 4 ? 1 : 2;
+    static constexpr int kWarpBytes = kStages * kStage;
+    static constexpr int kQOff = kD4Warps * kWarpBytes;
+    static constexpr int kQBytes = NT == 1 ? 0 : (D / 32) * NT * 32 * 16;  // Q fragments
+    static constexpr int kCtlOff = kQOff + kQBytes;
+    struct Ctl {
+        uint64_t full[kD4Warps][kStages];
+        unsigned long long sums[kD4Warps];
+        unsigned long long first;  // work before the sequence that holds this CTA's first tile
+        int b;                     // that sequence
+        uint32_t abort;
+    };
+    static constexpr int kBytes = kCtlOff + (int)sizeof(Ctl);
+    static_assert((kRows * D + 2 * kRows) * 4 <= kWarpBytes, "a warp merges through its ring");
+    static_assert(kTile % 16 == 0 && kStage % 16 == 0 && kCtlOff % 16 == 0, "bulk copies need 16 bytes");
+};
+
+// Tiles of one sequence: [first, first + n). A valid sequence has at least one, so that the
+// rows of an empty one are written too; one outside [0, capacity] has none.
+struct Dec4Seq {
+    int len, first, n;
+};
+__device__ __forceinline__ Dec4Seq dec4_seq(const Dec4Params& p, int b) {
+    Dec4Seq s;
+    s.len = __ldg(p.seqlens + b);
+    s.first = s.n = 0;
+    if (s.len < 0 || s.len > p.capacity) return s;
+    const long long lo = p.window > 0 ? (long long)s.len - p.Tq - p.window + 1 : 0;
+    s.first = lo > 0 ? (int)(lo / kD4Keys) : 0;
+    s.n = max(1, (s.len + kD4Keys - 1) / kD4Keys - s.first);
+    return s;
+}
+
+// Start of CTA i's run when `total` tiles are cut into `ctas` runs.
+__device__ __forceinline__ unsigned long long dec4_cut(unsigned long long total, unsigned i, unsigned ctas) {
+    return total * i / ctas;  // total is below 2^52 (checked on the host), i a few hundred
+}
+
+// Two codes as bf16 numbers 16 + c: nibble e of the low half and of the high half.
+template <int e>
+__device__ __forceinline__ uint32_t dec4_codes(uint32_t w) {
+    const uint32_t x = e == 0 ? w << 3 : w >> (4 * e - 3);
+    return (x & 0x00780078u) | 0x41804180u;
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+// All threads of the block: the sum over sequences of f(b), and the sum over b < upto.
+template <int kWarps, class F>
+__device__ __forceinline__ void dec4_sums(int B, int upto, unsigned long long* warp_sums, F f, unsigned long long* before,
+                                          unsigned long long* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned long long v[2] = {0, 0};
+    for (int b = threadIdx.x; b < B; b += 32 * kWarps) {
+        const unsigned long long x = f(b);
+        v[0] += x;
+        if (b < upto) v[1] += x;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+        if (lane == 0) warp_sums[warp] = v[i];
+        __syncthreads();
+        v[i] = 0;
+        for (int w = 0; w < kWarps; ++w) v[i] += warp_sums[w];
+        __syncthreads();
+    }
+    *total = v[0];
+    *before = v[1];
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kD4Threads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_decode_kv4_kernel(const Dec4Params p) {
+    using C = Dec4Cfg<D, NT>;
+    constexpr int kStages = C::kStages;
+    constexpr int RW = C::kRow / 4;  // words of a stored row
+    constexpr int kKI = D / 32;      // word groups of a key row: four words, one a lane of a quad
+    constexpr int kVI = D / 64;      // word groups of a value row: eight words, one a quad
+    constexpr int kMT = D / 16;      // m16 tiles of the output's d
+    extern __shared__ __align__(16) uint8_t dec4_smem[];
+    typename C::Ctl* ctl = reinterpret_cast<typename C::Ctl*>(dec4_smem + C::kCtlOff);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    uint8_t* ring = dec4_smem + warp * C::kWarpBytes;
+    const uint32_t ring_addr = smem_u32(ring);
+    const uint32_t bars = smem_u32(&ctl->full[warp][0]);
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
+        if (warp == 0) ctl->abort = 0;
+        fence_mbar_init();
+    }
+
+    // ---- this CTA's run of tiles and the sequence it starts in
+    const int units = p.Hkv * p.n_rc;  // units of a sequence
+    const auto work_of = [&](int b) { return (unsigned long long)dec4_seq(p, b).n * units; };
+    unsigned long long total, before;
+    dec4_sums<kD4Warps>(p.B, 0, ctl->sums, work_of, &before, &total);
+    const unsigned ctas = (unsigned)min((unsigned long long)gridDim.x, total);
+    if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b < p.B; b += kD4Threads)
+            if (dec4_seq(p, b).n == 0) atomicOr(p.err, kDevErrBadSeqlens);
+    if (blockIdx.x >= ctas) return;
+    unsigned long long at = dec4_cut(total, blockIdx.x, ctas);
+    const unsigned long long end = dec4_cut(total, blockIdx.x + 1, ctas);
+    {
+        unsigned long long run = 0;  // work before this round's sequences
+        for (int b0 = 0; b0 < p.B && run <= at; b0 += kD4Threads) {
+            const int b = b0 + threadIdx.x;
+            const unsigned long long x = b < p.B ? work_of(b) : 0;
+            unsigned long long inc = x;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += y;
+            }
+            if (lane == 31) ctl->sums[warp] = inc;
+            __syncthreads();
+            unsigned long long base = run;
+            for (int w = 0; w < warp; ++w) base += ctl->sums[w];
+            const unsigned long long lo = base + inc - x;
+            if (x > 0 && lo <= at && at < lo + x) {
+                ctl->b = b;
+                ctl->first = lo;
+            }
+            for (int w = 0; w < kD4Warps; ++w) run += ctl->sums[w];
+            __syncthreads();
+        }
+    }
+    int b = ctl->b;
+    unsigned long long seq0 = ctl->first;
+    Dec4Seq s = dec4_seq(p, b);
+
+    const float sl2 = p.scale_log2;
+    const int box = min(p.page_size, kD4Keys);  // rows of one bulk copy
+    const int boxes = kD4Keys / box;            // 1, or 2 for pages of 16 rows
+    volatile uint32_t* abort_flag = &ctl->abort;
+    int stage = 0;
+    uint32_t phase = 0;
+
+    while (at < end) {
+        while (at >= seq0 + (unsigned long long)s.n * units) {  // sequences without work have n = 0
+            seq0 += (unsigned long long)s.n * units;
+            s = dec4_seq(p, ++b);
+        }
+        // ---- the piece: tiles [t0, t1) of unit u of sequence b
+        const unsigned long long in_seq = at - seq0;
+        const int u = (int)(in_seq / (unsigned)s.n);
+        const int t0 = (int)(in_seq - (unsigned long long)u * s.n);
+        const int t1 = (int)min((unsigned long long)s.n, t0 + (end - at));
+        at += t1 - t0;
+        const int h = u / p.n_rc, rc = u - h * p.n_rc;
+        const int rbase = rc * C::kRows;
+        const int nrows = min(C::kRows, p.G * p.Tq - rbase);
+        const size_t row0 = ((size_t)b * p.Hq + (size_t)h * p.G) * p.Tq + rbase;
+        const int key_base = (s.first + t0) * kD4Keys;
+        const int n_mine = (t1 - t0 - warp + kD4Warps - 1) / kD4Warps;  // tiles warp, warp + kD4Warps, ...
+        const uint8_t* k_head = p.k + h * p.k_sh;
+        const uint8_t* v_head = p.v + h * p.v_sh;
+
+        // Pool page of this lane's box of the warp's tile i.
+        const auto look_up = [&](int i) {
+            const int key = key_base + (warp + i * kD4Warps) * kD4Keys + lane * box;
+            return i < n_mine && lane < boxes && key < s.len ? __ldg(p.table + (size_t)b * p.max_pages + key / p.page_size)
+                                                             : -1;
+        };
+        // Copy the warp's tile i into ring stage st. Boxes past the sequence are left out (their
+        // keys are masked); a page number outside the pool reads as rows of zeros.
+        const auto fetch = [&](int i, int st, int page) {
+            const int key = key_base + (warp + i * kD4Warps) * kD4Keys + lane * box;
+            const bool want = lane < boxes && key < s.len;
+            const bool ok = want && page >= 0 && page < p.num_pages;
+            const unsigned oks = __ballot_sync(0xffffffffu, ok), wants = __ballot_sync(0xffffffffu, want);
+            const uint32_t bar = bars + 8 * st, dst = ring_addr + st * C::kStage + lane * box * C::kRow;
+            if (lane == 0) mbar_arrive_expect_tx(bar, __popc(oks) * 2 * box * C::kRow);
+            __syncwarp();
+            if (ok) {
+                const long long row = (long long)(key % p.page_size) * C::kRow;
+                bulk_load(dst, k_head + page * p.k_sb + row, box * C::kRow, bar);
+                bulk_load(dst + C::kTile, v_head + page * p.v_sb + row, box * C::kRow, bar);
+            }
+            if (oks != wants) {
+                for (int x = 0; x < boxes; ++x)
+                    if ((wants & ~oks) >> x & 1u)
+                        for (int e = lane; e < box * RW; e += 32) {
+                            uint32_t* z = reinterpret_cast<uint32_t*>(ring + st * C::kStage + x * box * C::kRow) + e;
+                            z[0] = z[C::kTile / 4] = 0u;
+                        }
+                fence_proxy_async_smem();  // before a later copy into these bytes
+            }
+        };
+        int page = look_up(0);
+        for (int i = 0, st = stage; i < kStages && i < n_mine; ++i) {
+            fetch(i, st, page);
+            page = look_up(i + 1);
+            st = st + 1 == kStages ? 0 : st + 1;
+        }
+
+        // ---- Q fragments: lane (g, t) holds words t + 4i of row g's elements, as pairs (e, e + 4)
+        uint4 qf[NT == 1 ? kKI : 1];
+        float sumq[NT][2];  // sums of the rows 2t, 2t + 1 of each tile
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float sum = 0.f;
+            const bool row_ok = 8 * nt + g < nrows;
+#pragma unroll
+            for (int i = 0; i < kKI; ++i) {
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (row_ok) x = *reinterpret_cast<const uint4*>(p.q + (row0 + 8 * nt + g) * D + 8 * (t + 4 * i));
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    sum += __uint_as_float(w[e] << 16) + __uint_as_float(w[e] & 0xffff0000u);
+                const uint4 f = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                                           __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+                if constexpr (NT == 1)
+                    qf[i] = f;
+                else if (warp == 0)
+                    reinterpret_cast<uint4*>(dec4_smem + C::kQOff)[(i * NT + nt) * 32 + lane] = f;
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            sumq[nt][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
+            sumq[nt][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        }
+        if constexpr (NT > 1) __syncthreads();
+
+        float m[NT][2], l[NT][2], beta[NT][2];
+        float oacc[kMT][NT][4], ones[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = beta[nt][0] = beta[nt][1] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                ones[nt][e] = 0.f;
+#pragma unroll
+                for (int i = 0; i < kMT; ++i) oacc[i][nt][e] = 0.f;
+            }
+        }
+        const int pos_min = s.len - p.Tq;                                          // position of row 0
+        const int lo_max = p.window > 0 ? s.len - min(p.window, s.len) : -1;  // first key of the last row
+
+        for (int it = 0; it < n_mine; ++it) {
+            const bool ready = mbar_wait_bounded(bars + 8 * stage, phase, abort_flag, p.err, p.timeout_ns);
+            if (!__all_sync(0xffffffffu, ready)) {
+                // let the copies that are under way land: the later stages, oldest first
+                int st = stage;
+                uint32_t ph = phase;
+                for (int i = it; i < n_mine && i < it + kStages; ++i) {
+                    mbar_wait_drain(bars + 8 * st, ph, p.timeout_ns);
+                    if (++st == kStages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+                break;
+            }
+            const uint32_t* K = reinterpret_cast<const uint32_t*>(ring + stage * C::kStage);
+            const uint32_t* V = K + C::kTile / 4;
+            const int key0 = key_base + (warp + it * kD4Warps) * kD4Keys;
+            // ---- S^T = K Q^T: accumulator rows g, g + 8 are keys 4g + 2mt, 4g + 2mt + 1
+            float sacc[2][NT][4];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    sacc[mt][nt][0] = sacc[mt][nt][2] = -16.f * sumq[nt][0];
+                    sacc[mt][nt][1] = sacc[mt][nt][3] = -16.f * sumq[nt][1];
+                }
+            const uint32_t* kr = K + 4 * g * RW + t;
+#pragma unroll
+            for (int i = 0; i < kKI; ++i) {
+                uint4 f[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if constexpr (NT == 1)
+                        f[nt] = qf[i];
+                    else
+                        f[nt] = reinterpret_cast<const uint4*>(dec4_smem + C::kQOff)[(i * NT + nt) * 32 + lane];
+                }
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    const uint32_t w0 = kr[(2 * mt) * RW + 4 * i], w1 = kr[(2 * mt + 1) * RW + 4 * i];
+                    const uint32_t a[4] = {dec4_codes<0>(w0), dec4_codes<0>(w1), dec4_codes<1>(w0), dec4_codes<1>(w1)};
+                    const uint32_t c[4] = {dec4_codes<2>(w0), dec4_codes<2>(w1), dec4_codes<3>(w0), dec4_codes<3>(w1)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_bf16_16816(sacc[mt][nt], a, f[nt].x, f[nt].y);
+                        mma_bf16_16816(sacc[mt][nt], c, f[nt].z, f[nt].w);
+                    }
+                }
+            }
+            // ---- scores in log2 units
+            const bool masked = key0 + kD4Keys > pos_min + 1 || key0 < lo_max;
+            float kscale[4], kmin[4], vscale[4], vmid[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t kh = K[(4 * g + c) * RW + D / 8], vh = V[(4 * g + c) * RW + D / 8];
+                kscale[c] = __uint_as_float(kh << 16) * sl2;
+                kmin[c] = __uint_as_float(kh & 0xffff0000u) * sl2;
+                vscale[c] = __uint_as_float(vh << 16);
+                vmid[c] = fmaf(8.f, vscale[c], __uint_as_float(vh & 0xffff0000u));
+            }
+            bool raise = false;
+            float m_new[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    int hi = 0x7fffffff, lo = -1;  // keys this row sees, in the tile's numbering
+                    if (masked) {
+                        const int pos = s.len - p.Tq + (rbase + 8 * nt + 2 * t + x) % p.Tq;
+                        hi = pos - key0;
+                        lo = p.window > 0 ? hi - p.window + 1 : -1;
+                    }
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float& sc = sacc[c >> 1][nt][(c & 1) * 2 + x];
+                        sc = fmaf(sc, kscale[c], kmin[c] * sumq[nt][x]);
+                        if (masked && (4 * g + c > hi || 4 * g + c < lo)) sc = -INFINITY;
+                        mx = fmaxf(mx, sc);
+                    }
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    m_new[nt][x] = fmaxf(m[nt][x], mx);
+                    raise |= m_new[nt][x] > m[nt][x];
+                }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float alpha = m_new[nt][x] > m[nt][x] ? ex2_approx(m[nt][x] - m_new[nt][x]) : 1.f;
+                        m[nt][x] = m_new[nt][x];
+                        l[nt][x] *= alpha;
+                        beta[nt][x] *= alpha;
+                        ones[nt][x] *= alpha;  // its four rows are alike: only the first two are used
+#pragma unroll
+                        for (int i = 0; i < kMT; ++i) {
+                            oacc[i][nt][x] *= alpha;
+                            oacc[i][nt][x + 2] *= alpha;
+                        }
+                    }
+            }
+            uint32_t pb[NT][4];  // B operand: keys 8t + c and 8t + 4 + c of query row g
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float w[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float sc = sacc[c >> 1][nt][(c & 1) * 2 + x];
+                        const float mu = m[nt][x] == -INFINITY ? 0.f : m[nt][x];
+                        const float e = ex2_approx(sc - mu);
+                        l[nt][x] += e;
+                        w[x] = e * vscale[c];
+                        float y = e * vmid[c];
+                        if (masked && sc == -INFINITY) w[x] = y = 0.f;  // such a key's scale may be NaN
+                        beta[nt][x] += y;
+                    }
+                    pb[nt][c] = movmatrix_trans(pack_bf16x2(w[0], w[1]));
+                }
+            // ---- O^T += V^T P^T
+            const uint32_t* vr = V + 8 * t * RW + g;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                uint32_t lo[2][kVI], hi[2][kVI];
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < kVI; ++i) {
+                        const uint32_t x = vr[(2 * ks + c) * RW + 8 * i], y = vr[(2 * ks + c + 4) * RW + 8 * i];
+                        lo[c][i] = __byte_perm(x, y, 0x5410);
+                        hi[c][i] = __byte_perm(x, y, 0x7632);
+                    }
+                const auto product = [&](float (&acc)[NT][4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                    const uint32_t a[4] = {a0, a1, a2, a3};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(acc[nt], a, pb[nt][2 * ks], pb[nt][2 * ks + 1]);
+                };
+                constexpr uint32_t kOne = 0x3F803F80u;
+                product(ones, kOne, kOne, kOne, kOne);
+                if constexpr (D == 128) {  // rows g, g + 8 of tile e: d = 8g + e, 64 + 8g + e
+#define GQA_D4_HALF(x, e, tile) \
+    product(oacc[tile], dec4_codes<e>(x[0][0]), dec4_codes<e>(x[0][1]), dec4_codes<e>(x[1][0]), dec4_codes<e>(x[1][1]))
+                    GQA_D4_HALF(lo, 0, 0);
+                    GQA_D4_HALF(lo, 1, 1);
+                    GQA_D4_HALF(lo, 2, 2);
+                    GQA_D4_HALF(lo, 3, 3);
+                    GQA_D4_HALF(hi, 0, 4);
+                    GQA_D4_HALF(hi, 1, 5);
+                    GQA_D4_HALF(hi, 2, 6);
+                    GQA_D4_HALF(hi, 3, 7);
+#undef GQA_D4_HALF
+                } else {  // rows g, g + 8 of tile e: d = 8g + e, 8g + 4 + e
+#define GQA_D4_ALL(e) \
+    product(oacc[e], dec4_codes<e>(lo[0][0]), dec4_codes<e>(hi[0][0]), dec4_codes<e>(lo[1][0]), dec4_codes<e>(hi[1][0]))
+                    GQA_D4_ALL(0);
+                    GQA_D4_ALL(1);
+                    GQA_D4_ALL(2);
+                    GQA_D4_ALL(3);
+#undef GQA_D4_ALL
+                }
+            }
+            __syncwarp();  // every lane has read the stage
+            if (it + kStages < n_mine) {
+                fetch(it + kStages, stage, page);
+                page = look_up(it + kStages + 1);
+            }
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+
+        // ---- merge the warps' states, each through its own ring (all its copies are consumed)
+        float* area = reinterpret_cast<float*>(ring);  // m[rows], l[rows], O[rows][D]
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], d);
+                    beta[nt][x] += __shfl_xor_sync(0xffffffffu, beta[nt][x], d);
+                }
+                const int n = 8 * nt + 2 * t + x;
+                if (g == 0) {
+                    area[n] = m[nt][x];
+                    area[C::kRows + n] = l[nt][x];
+                }
+                const float shift = fmaf(-24.f, ones[nt][x], beta[nt][x]);
+                float* out = area + 2 * C::kRows + n * D + 8 * g;
+#pragma unroll
+                for (int i = 0; i < kMT; ++i) {
+                    out[i] = oacc[i][nt][x] + shift;
+                    out[(D == 128 ? 64 : 4) + i] = oacc[i][nt][x + 2] + shift;
+                }
+            }
+        __syncthreads();
+        if (*abort_flag) return;  // uniform: the flag is set before the barrier and never cleared
+        const bool whole = t0 == 0 && t1 == s.n;
+        const size_t slot = 2 * (size_t)blockIdx.x + (t0 > 0 ? 0 : 1);
+        for (int idx = threadIdx.x; idx < nrows * D; idx += kD4Threads) {
+            const int row = idx / D, d = idx - row * D;
+            constexpr int kStep = C::kWarpBytes / 4;
+            const float* base = reinterpret_cast<const float*>(dec4_smem);
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kD4Warps; ++w) M = fmaxf(M, base[w * kStep + row]);
+            const float mu = M == -INFINITY ? 0.f : M;
+            float sum = 0.f, acc = 0.f;
+#pragma unroll
+            for (int w = 0; w < kD4Warps; ++w) {
+                const float f = ex2_approx(base[w * kStep + row] - mu);
+                sum += base[w * kStep + C::kRows + row] * f;
+                acc += base[w * kStep + 2 * C::kRows + row * D + d] * f;
+            }
+            // a row that sees no key of the piece: 0, and weight 0 in a later merge (NaN stays NaN)
+            const float val = sum == 0.f ? 0.f : acc / sum;
+            if (whole) {
+                p.o[(row0 + row) * D + d] = __float2bfloat16_rn(val);
+            } else {
+                p.part[(slot * C::kRows + row) * D + d] = val;
+                if (d == 0) p.part_lse[slot * C::kRows + row] = sum == 0.f ? -INFINITY : M + __log2f(sum);
+            }
+        }
+        fence_proxy_async_smem();  // the areas are read before the next piece's copies land on them
+        __syncthreads();
+    }
+}
+
+// Merge the pieces of the units that were cut between CTAs, in CTA order: one block a unit, one
+// warp a row. The cuts are computed again from the lengths.
+template <int D, int NT>
+__global__ void __launch_bounds__(kD4Threads) gqa_decode_kv4_merge_kernel(const Dec4Params p, unsigned grid) {
+    constexpr int kRows = 8 * NT;
+    constexpr int E = D / 32;
+    __shared__ unsigned long long sums[kD4Warps];
+    const int units = p.Hkv * p.n_rc;
+    const int b = blockIdx.x / units, u = blockIdx.x - b * units;
+    unsigned long long total, before;
+    dec4_sums<kD4Warps>(
+        p.B, b, sums, [&](int i) { return (unsigned long long)dec4_seq(p, i).n * units; }, &before, &total);
+    const int n = dec4_seq(p, b).n;
+    if (n == 0) return;
+    const unsigned ctas = (unsigned)min((unsigned long long)grid, total);
+    const unsigned long long first = before + (unsigned long long)u * n, last = first + n - 1;
+    // the CTA of tile w is the last one whose run starts at or before w
+    const unsigned c0 = (unsigned)(((first + 1) * ctas - 1) / total), c1 = (unsigned)(((last + 1) * ctas - 1) / total);
+    if (c0 == c1) return;
+    const int h = u / p.n_rc, rbase = (u - h * p.n_rc) * kRows;
+    const int nrows = min(kRows, p.G * p.Tq - rbase);
+    const int lane = threadIdx.x & 31;
+    for (int row = threadIdx.x >> 5; row < nrows; row += kD4Warps) {
+        // the first piece starts the unit (slot 1 of its CTA), the others do not (slot 0)
+        const auto at = [&](unsigned c) { return (2 * (size_t)c + (c == c0 ? 1 : 0)) * kRows + row; };
+        float M = -INFINITY;
+        for (unsigned c = c0; c <= c1; ++c) M = fmaxf(M, p.part_lse[at(c)]);
+        const float mu = M == -INFINITY ? 0.f : M;
+        float sum = 0.f, acc[E] = {};
+        for (unsigned c = c0; c <= c1; ++c) {
+            const float f = ex2_approx(p.part_lse[at(c)] - mu);
+            sum += f;
+            const float* src = p.part + at(c) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += f * src[e];
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        __nv_bfloat16* out = p.o + (((size_t)b * p.Hq + (size_t)h * p.G) * p.Tq + rbase + row) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    }
+}
+
+}  // namespace gqa

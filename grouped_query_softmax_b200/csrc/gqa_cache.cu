@@ -1,0 +1,485 @@
+// The operators around a paged key/value cache (declared in include/gqa.h): the plan of a step,
+// the norm and rotation of queries and keys with its gradients and its cache-writing form, the
+// rows of a cache held in 4 bits, and decode over that cache. Argument checks and launches; the
+// kernels are in paged_plan.cuh, rope_sm100.cuh, kv4_rows_sm100.cuh and decode_kv4_sm100.cuh.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/gqa.h"
+#include "decode_kv4_sm100.cuh"
+#include "gqa_internal.h"
+#include "kv4_rows_sm100.cuh"
+#include "paged_plan.cuh"
+#include "rope_sm100.cuh"
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+bool aligned(const void* p, uintptr_t n) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool aligned_or_null(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Pages the attention calls read, and rows that fit the 32-bit slot numbers.
+gqa_status check_pages(int page_size, int num_pages) {
+    const bool ok = page_size >= 16 && page_size % 16 == 0 &&
+                    (page_size % gqa::kTileKeys == 0 || gqa::kTileKeys % page_size == 0);
+    if (!ok || num_pages <= 0) return GQA_ERR_INVALID_ARGUMENT;
+    return (long long)page_size * num_pages <= 0x7fffffffLL ? GQA_OK : GQA_ERR_UNSUPPORTED;
+}
+
+// Element strides of rows that are read or written 8 or 16 bytes at a time. A stride along an
+// axis of extent 1 is not used.
+gqa_status check_rows(const gqa_layout* l, int B, int H, int T, int D, long long* sb, long long* sh, long long* st) {
+    if (l == nullptr) return GQA_ERR_INVALID_ARGUMENT;
+    *sb = B > 1 ? l->sb : 0;
+    *sh = H > 1 ? l->sh : 0;
+    *st = T > 1 ? l->st : 0;
+    if ((B > 1 && *sb <= 0) || (H > 1 && *sh <= 0) || (T > 1 && *st < D)) return GQA_ERR_INVALID_ARGUMENT;
+    if ((*sb | *sh | *st) & 7) return GQA_ERR_INVALID_ARGUMENT;
+    return GQA_OK;
+}
+
+gqa_status check_heads(int Hq, int Hkv, int D) {
+    if (Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0) return GQA_ERR_INVALID_ARGUMENT;
+    return D == 64 || D == 128 ? GQA_OK : GQA_ERR_UNSUPPORTED;
+}
+
+gqa_status launched(cudaError_t e) { return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA; }
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+        sms = 148;
+    return sms;
+}
+
+// ---------------------------------------------------------------- norm and rotation
+gqa_status rope_params(gqa::RopeParams& p, const gqa_rope* r, int B, int T, int Hq, int Hkv, int D) {
+    gqa_status st = check_heads(Hq, Hkv, D);
+    if (st != GQA_OK) return st;
+    if (r == nullptr || B <= 0 || T <= 0) return GQA_ERR_INVALID_ARGUMENT;
+    if ((long long)B * T > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
+    p.x[0].weight = r->q_weight;
+    p.x[1].weight = r->k_weight;
+    p.weight_fp32 = r->weight_fp32 != 0;
+    if (!aligned_or_null(r->q_weight, p.weight_fp32 ? 4 : 2) || !aligned_or_null(r->k_weight, p.weight_fp32 ? 4 : 2))
+        return GQA_ERR_INVALID_ARGUMENT;
+    if (!(r->eps >= 0.f) || std::isinf(r->eps)) return GQA_ERR_INVALID_ARGUMENT;
+    p.eps = r->eps;
+    if ((r->cos == nullptr) != (r->sin == nullptr)) return GQA_ERR_INVALID_ARGUMENT;
+    if (r->cos != nullptr) {
+        if (!aligned(r->cos, 16) || !aligned(r->sin, 16) || !aligned_or_null(r->positions, 4)) return GQA_ERR_INVALID_ARGUMENT;
+        if (r->rot < 8 || r->rot > D || r->rot % 8 != 0 || r->n_positions <= 0) return GQA_ERR_INVALID_ARGUMENT;
+        if (r->positions == nullptr && T > r->n_positions) return GQA_ERR_INVALID_ARGUMENT;
+        if (r->positions != nullptr && B > 1 && r->positions_sb < 0) return GQA_ERR_INVALID_ARGUMENT;
+        p.cos = r->cos;
+        p.sin = r->sin;
+        p.rot = r->rot;
+        p.n_positions = r->n_positions;
+        p.positions = r->positions;
+        p.pos_sb = B > 1 ? r->positions_sb : 0;
+    } else {
+        p.rot = D;  // lanes take the halves of the row; nothing turns
+    }
+    p.B = B;
+    p.T = T;
+    p.x[0].H = Hq;
+    p.x[1].H = Hkv;
+    return GQA_OK;
+}
+
+// Heads of a token that one team of D/8 lanes takes in turn: all its loads of the angles and
+// weights serve that many rows, so a large launch takes many; a small one takes few, to spread
+// over the SMs.
+int rope_heads_per_team(long long tokens, int heads, int D, int sms) {
+    const long long teams_at_8 = tokens * ((heads + 7) / 8);
+    return teams_at_8 * (D / 8) >= (long long)sms * 2048 ? 8 : 4;
+}
+
+template <int D>
+gqa_status rope_fwd(gqa::RopeParams p, bool interleaved, cudaStream_t stream) {
+    if ((p.err = gqa::device_error_ptr()) == nullptr) return GQA_ERR_CUDA;
+    const long long teams = (long long)p.B * p.T * (p.blocks[0] + p.blocks[1] + p.blocks[2]);
+    constexpr int kPer = gqa::kRopeThreads / (D / 8);
+    const long long ctas = (teams + kPer - 1) / kPer;
+    if (ctas > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
+    if (interleaved)
+        gqa::gqa_rope_fwd_kernel<D, true><<<(unsigned)ctas, gqa::kRopeThreads, 0, stream>>>(p);
+    else
+        gqa::gqa_rope_fwd_kernel<D, false><<<(unsigned)ctas, gqa::kRopeThreads, 0, stream>>>(p);
+    return launched(cudaGetLastError());
+}
+
+// CTAs of the backward pass: queries' first, then keys'. Each leaves one row of weight sums.
+struct RopeBwdPlan {
+    int heads_per_team, q_ctas, k_ctas;
+};
+RopeBwdPlan rope_bwd_plan(int B, int T, int Hq, int Hkv, int D) {
+    const int sms = sm_count();
+    RopeBwdPlan r;
+    r.heads_per_team = rope_heads_per_team((long long)B * T, Hq + Hkv, D, sms);
+    const int per_cta = gqa::kRopeThreads / (D / 8);
+    const auto ctas = [&](int H) {
+        const long long units = (long long)B * T * ((H + r.heads_per_team - 1) / r.heads_per_team);
+        const long long most = std::max<long long>(1, (long long)sms * 8 * H / (Hq + Hkv));
+        return (int)std::min<long long>((units + per_cta - 1) / per_cta, most);
+    };
+    r.q_ctas = ctas(Hq);
+    r.k_ctas = ctas(Hkv);
+    return r;
+}
+
+template <int D>
+gqa_status rope_bwd(gqa::RopeParams p, int ctas, bool interleaved, float* dq_weight, float* dk_weight,
+                    cudaStream_t stream) {
+    if ((p.err = gqa::device_error_ptr()) == nullptr) return GQA_ERR_CUDA;
+    if (interleaved)
+        gqa::gqa_rope_bwd_kernel<D, true><<<(unsigned)ctas, gqa::kRopeThreads, 0, stream>>>(p);
+    else
+        gqa::gqa_rope_bwd_kernel<D, false><<<(unsigned)ctas, gqa::kRopeThreads, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || (dq_weight == nullptr && dk_weight == nullptr)) return launched(e);
+    gqa::gqa_rope_dw_kernel<D><<<2, 1024, 0, stream>>>(p.partial, p.q_blocks, ctas, dq_weight, dk_weight);
+    return launched(cudaGetLastError());
+}
+
+// ---------------------------------------------------------------- 4-bit rows
+gqa_status check_kv4_pool(const void* pool, const gqa_kv4_layout* l, int num_pages, int Hkv, int page_size, int D,
+                          long long* sb, long long* sh) {
+    if (l == nullptr || !aligned(pool, 16)) return GQA_ERR_INVALID_ARGUMENT;
+    *sb = num_pages > 1 ? l->sb : 0;
+    *sh = Hkv > 1 ? l->sh : 0;
+    const long long rows = (long long)page_size * (D / 2 + 4);
+    if ((num_pages > 1 && *sb < rows) || (Hkv > 1 && *sh < rows)) return GQA_ERR_INVALID_ARGUMENT;
+    return ((*sb | *sh) & 15) ? GQA_ERR_INVALID_ARGUMENT : GQA_OK;
+}
+
+gqa_status kv4_rows(bool append, const void* k, const void* v, const void* k_pool, const void* v_pool, const int* slots,
+                    int N, int Hkv, int D, int page_size, int num_pages, const gqa_layout* k_layout,
+                    const gqa_layout* v_layout, const gqa_kv4_layout* k_pool_layout, const gqa_kv4_layout* v_pool_layout,
+                    void* stream) {
+    gqa_status st = check_heads(Hkv, Hkv, D);
+    if (st != GQA_OK) return st;
+    if (N < 0) return GQA_ERR_INVALID_ARGUMENT;
+    if ((st = check_pages(page_size, num_pages)) != GQA_OK) return st;
+    gqa::Kv4RowsParams p{};
+    if ((st = check_kv4_pool(k_pool, k_pool_layout, num_pages, Hkv, page_size, D, &p.x[0].pool_sb, &p.x[0].pool_sh)) != GQA_OK)
+        return st;
+    if ((st = check_kv4_pool(v_pool, v_pool_layout, num_pages, Hkv, page_size, D, &p.x[1].pool_sb, &p.x[1].pool_sh)) != GQA_OK)
+        return st;
+    if (N == 0) return GQA_OK;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return GQA_ERR_INVALID_ARGUMENT;
+    long long unused;
+    if ((st = check_rows(k_layout, 1, Hkv, N, D, &unused, &p.x[0].sh, &p.x[0].st)) != GQA_OK) return st;
+    if ((st = check_rows(v_layout, 1, Hkv, N, D, &unused, &p.x[1].sh, &p.x[1].st)) != GQA_OK) return st;
+    p.x[0].rows = static_cast<bf16*>(const_cast<void*>(k));
+    p.x[1].rows = static_cast<bf16*>(const_cast<void*>(v));
+    p.x[0].pool = static_cast<uint8_t*>(const_cast<void*>(k_pool));
+    p.x[1].pool = static_cast<uint8_t*>(const_cast<void*>(v_pool));
+    p.slots = slots;
+    p.N = N;
+    p.H = Hkv;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    if ((p.err = gqa::device_error_ptr()) == nullptr) return GQA_ERR_CUDA;
+    const int per = gqa::kKv4Threads / (D / 8);
+    const long long ctas = (2LL * N * Hkv + per - 1) / per;
+    if (ctas > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)ctas);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (append) {
+        if (D == 128)
+            gqa::gqa_kv4_append_kernel<128><<<grid, gqa::kKv4Threads, 0, s>>>(p);
+        else
+            gqa::gqa_kv4_append_kernel<64><<<grid, gqa::kKv4Threads, 0, s>>>(p);
+    } else {
+        if (D == 128)
+            gqa::gqa_kv4_gather_kernel<128><<<grid, gqa::kKv4Threads, 0, s>>>(p);
+        else
+            gqa::gqa_kv4_gather_kernel<64><<<grid, gqa::kKv4Threads, 0, s>>>(p);
+    }
+    return launched(cudaGetLastError());
+}
+
+// ---------------------------------------------------------------- decode over 4-bit rows
+constexpr int kMaxDecodeRows = 16;           // new queries a sequence
+constexpr int kDec4MaxKeys = 1 << 30;        // key numbers plus a tile stay below 2^31
+
+gqa_status check_dec4(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, int window) {
+    const gqa_status st = check_heads(Hq, Hkv, D);
+    if (st != GQA_OK) return st;
+    if (B <= 0 || Tq <= 0 || max_seqlen_k <= 0 || window < 0) return GQA_ERR_INVALID_ARGUMENT;
+    if (Tq > kMaxDecodeRows || max_seqlen_k > kDec4MaxKeys) return GQA_ERR_UNSUPPORTED;
+    // blocks of the merge in 31 bits; tiles of all units in 52, times the CTAs in 64
+    const long long rows = (long long)B * Hq * Tq;
+    if (rows > 0x7fffffffLL || rows * (max_seqlen_k / gqa::kD4Keys + 2) >= 1LL << 52) return GQA_ERR_UNSUPPORTED;
+    return GQA_OK;
+}
+
+// N tiles of 8 query rows a CTA takes: as few as hold a group's rows, four at most.
+int dec4_nt(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+struct Dec4Plan {
+    int nt, n_rc, ctas;
+};
+Dec4Plan dec4_plan(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, int window) {
+    Dec4Plan r;
+    const int rows = Hq / Hkv * Tq;
+    r.nt = dec4_nt(rows);
+    r.n_rc = (rows + 8 * r.nt - 1) / (8 * r.nt);
+    const int per_sm = r.nt == 4 ? 1 : 2;
+    // no more CTAs than the longest lengths would give a tile for each warp
+    const long long keys = window > 0 ? std::min<long long>(max_seqlen_k, (long long)window + Tq + gqa::kD4Keys) : max_seqlen_k;
+    const long long tiles = (keys + gqa::kD4Keys - 1) / gqa::kD4Keys;
+    const long long most = ((long long)B * Hkv * r.n_rc * tiles + gqa::kD4Warps - 1) / gqa::kD4Warps;
+    r.ctas = (int)std::min<long long>((long long)sm_count() * per_sm, most);
+    return r;
+}
+size_t dec4_lse_offset(const Dec4Plan& r, int D) { return gqa::round256((size_t)2 * r.ctas * 8 * r.nt * D * sizeof(float)); }
+size_t dec4_bytes(const Dec4Plan& r, int D) {
+    return dec4_lse_offset(r, D) + (size_t)2 * r.ctas * 8 * r.nt * sizeof(float);
+}
+
+template <int D, int NT>
+gqa_status launch_dec4(const gqa::Dec4Params& p, int ctas, cudaStream_t stream) {
+    using C = gqa::Dec4Cfg<D, NT>;
+    cudaError_t e = cudaFuncSetAttribute(gqa::gqa_decode_kv4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         C::kBytes);
+    if (e != cudaSuccess) return GQA_ERR_CUDA;
+    gqa::gqa_decode_kv4_kernel<D, NT><<<(unsigned)ctas, gqa::kD4Threads, C::kBytes, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess || ctas == 1) return launched(e);
+    gqa::gqa_decode_kv4_merge_kernel<D, NT>
+        <<<(unsigned)(p.B * p.Hkv * p.n_rc), gqa::kD4Threads, 0, stream>>>(p, (unsigned)ctas);
+    return launched(cudaGetLastError());
+}
+
+}  // namespace
+
+extern "C" {
+
+gqa_status gqa_paged_plan(const int* seqlens, const int* keep, const int* new_tokens, int* block_table, int* free_list,
+                          const int* free_count, int* seqlens_out, int* cu_seqlens, int* positions, int* slots,
+                          int* free_count_out, int S, int max_pages, int page_size, int num_pages, int free_capacity,
+                          int max_tokens, void* stream) {
+    if (S <= 0 || max_pages <= 0 || free_capacity <= 0 || max_tokens <= 0) return GQA_ERR_INVALID_ARGUMENT;
+    gqa_status st = check_pages(page_size, num_pages);
+    if (st != GQA_OK) return st;
+    if (S > gqa::kPagedMaxSeqs || (long long)max_pages * page_size > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
+    if (!aligned(seqlens, 4) || !aligned_or_null(keep, 4) || !aligned(new_tokens, 4) || !aligned(block_table, 4) ||
+        !aligned(free_list, 4) || !aligned(free_count, 4) || !aligned(seqlens_out, 4) || !aligned(cu_seqlens, 4) ||
+        !aligned(positions, 16) || !aligned(slots, 16) || !aligned(free_count_out, 4))
+        return GQA_ERR_INVALID_ARGUMENT;
+    gqa::PagedPlanParams p{seqlens, keep,      new_tokens, block_table, free_list,  free_count, seqlens_out, cu_seqlens,
+                           positions, slots,   free_count_out, S,       max_pages,  page_size,  num_pages,   free_capacity,
+                           max_tokens, gqa::device_error_ptr()};
+    if (p.err == nullptr) return GQA_ERR_CUDA;
+    const size_t smem = gqa::paged_plan_smem(S);
+    cudaError_t e = cudaSuccess;
+    if (smem > 48 * 1024 - 1024)  // beside the kernel's static shared memory
+        e = cudaFuncSetAttribute(gqa::gqa_paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)gqa::paged_plan_smem(gqa::kPagedMaxSeqs));
+    if (e != cudaSuccess) return GQA_ERR_CUDA;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = max_tokens > gqa::kPagedTokensAlone ? gqa::kPagedCluster : 1;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(attr.val.clusterDim.x);
+    cfg.blockDim = dim3(gqa::kPagedThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return launched(cudaLaunchKernelEx(&cfg, gqa::gqa_paged_plan_kernel, p));
+}
+
+gqa_status gqa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int T, int Hq, int Hkv, int D,
+                            const gqa_layout* q_layout, const gqa_layout* k_layout, const gqa_layout* q_out_layout,
+                            const gqa_layout* k_out_layout, const gqa_rope* rope, void* stream) {
+    gqa::RopeParams p{};
+    gqa_status st = rope_params(p, rope, B, T, Hq, Hkv, D);
+    if (st != GQA_OK) return st;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16)) return GQA_ERR_INVALID_ARGUMENT;
+    gqa::RopeRows &x = p.x[0], &y = p.x[1];
+    if ((st = check_rows(q_layout, B, Hq, T, D, &x.in_sb, &x.in_sh, &x.in_st)) != GQA_OK) return st;
+    if ((st = check_rows(k_layout, B, Hkv, T, D, &y.in_sb, &y.in_sh, &y.in_st)) != GQA_OK) return st;
+    if ((st = check_rows(q_out_layout, B, Hq, T, D, &x.out_sb, &x.out_sh, &x.out_st)) != GQA_OK) return st;
+    if ((st = check_rows(k_out_layout, B, Hkv, T, D, &y.out_sb, &y.out_sh, &y.out_st)) != GQA_OK) return st;
+    x.in = static_cast<const bf16*>(q);
+    y.in = static_cast<const bf16*>(k);
+    x.out = static_cast<bf16*>(q_out);
+    y.out = static_cast<bf16*>(k_out);
+    p.heads_per_team = rope_heads_per_team((long long)B * T, Hq + Hkv, D, sm_count());
+    p.blocks[0] = (Hq + p.heads_per_team - 1) / p.heads_per_team;
+    p.blocks[1] = (Hkv + p.heads_per_team - 1) / p.heads_per_team;
+    const bool inter = rope->interleaved != 0;
+    return D == 128 ? rope_fwd<128>(p, inter, static_cast<cudaStream_t>(stream))
+                    : rope_fwd<64>(p, inter, static_cast<cudaStream_t>(stream));
+}
+
+gqa_status gqa_qk_norm_rope_append(const void* q, const void* k, const void* v, void* q_out, void* k_pool, void* v_pool,
+                                   const int* slots, int N, int Hq, int Hkv, int D, int page_size, int num_pages,
+                                   const gqa_layout* q_layout, const gqa_layout* k_layout, const gqa_layout* v_layout,
+                                   const gqa_layout* q_out_layout, const gqa_layout* k_pool_layout,
+                                   const gqa_layout* v_pool_layout, const gqa_rope* rope, void* stream) {
+    if (N < 0) return GQA_ERR_INVALID_ARGUMENT;
+    gqa::RopeParams p{};
+    gqa_status st = rope_params(p, rope, 1, N > 0 ? N : 1, Hq, Hkv, D);
+    if (st != GQA_OK) return st;
+    if ((st = check_pages(page_size, num_pages)) != GQA_OK) return st;
+    if (!aligned(k_pool, 16) || !aligned(v_pool, 16)) return GQA_ERR_INVALID_ARGUMENT;
+    gqa::RopeRows &x = p.x[0], &y = p.x[1], &z = p.x[2];
+    z.H = Hkv;
+    if ((st = check_rows(k_pool_layout, num_pages, Hkv, page_size, D, &y.out_sb, &y.out_sh, &y.out_st)) != GQA_OK) return st;
+    if ((st = check_rows(v_pool_layout, num_pages, Hkv, page_size, D, &z.out_sb, &z.out_sh, &z.out_st)) != GQA_OK) return st;
+    if (N == 0) return GQA_OK;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(slots, 4))
+        return GQA_ERR_INVALID_ARGUMENT;
+    if ((st = check_rows(q_layout, 1, Hq, N, D, &x.in_sb, &x.in_sh, &x.in_st)) != GQA_OK) return st;
+    if ((st = check_rows(k_layout, 1, Hkv, N, D, &y.in_sb, &y.in_sh, &y.in_st)) != GQA_OK) return st;
+    if ((st = check_rows(v_layout, 1, Hkv, N, D, &z.in_sb, &z.in_sh, &z.in_st)) != GQA_OK) return st;
+    if ((st = check_rows(q_out_layout, 1, Hq, N, D, &x.out_sb, &x.out_sh, &x.out_st)) != GQA_OK) return st;
+    x.in = static_cast<const bf16*>(q);
+    y.in = static_cast<const bf16*>(k);
+    z.in = static_cast<const bf16*>(v);
+    x.out = static_cast<bf16*>(q_out);
+    y.out = static_cast<bf16*>(k_pool);
+    z.out = static_cast<bf16*>(v_pool);
+    p.slots = slots;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    p.heads_per_team = rope_heads_per_team(N, Hq + 2 * Hkv, D, sm_count());
+    p.blocks[0] = (Hq + p.heads_per_team - 1) / p.heads_per_team;
+    p.blocks[1] = p.blocks[2] = (Hkv + p.heads_per_team - 1) / p.heads_per_team;
+    const bool inter = rope->interleaved != 0;
+    return D == 128 ? rope_fwd<128>(p, inter, static_cast<cudaStream_t>(stream))
+                    : rope_fwd<64>(p, inter, static_cast<cudaStream_t>(stream));
+}
+
+size_t gqa_qk_norm_rope_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
+    if (check_heads(Hq, Hkv, D) != GQA_OK || B <= 0 || T <= 0) return 0;
+    const RopeBwdPlan r = rope_bwd_plan(B, T, Hq, Hkv, D);
+    return gqa::round256((size_t)(r.q_ctas + r.k_ctas) * D * sizeof(float));
+}
+
+gqa_status gqa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, void* dq, void* dk,
+                                float* dq_weight, float* dk_weight, int B, int T, int Hq, int Hkv, int D,
+                                const gqa_layout* dq_out_layout, const gqa_layout* dk_out_layout,
+                                const gqa_layout* q_layout, const gqa_layout* k_layout, const gqa_layout* dq_layout,
+                                const gqa_layout* dk_layout, const gqa_rope* rope, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+    gqa::RopeParams p{};
+    gqa_status st = rope_params(p, rope, B, T, Hq, Hkv, D);
+    if (st != GQA_OK) return st;
+    if (!aligned(dq_out, 16) || !aligned(dk_out, 16) || !aligned(dq, 16) || !aligned(dk, 16))
+        return GQA_ERR_INVALID_ARGUMENT;
+    gqa::RopeRows &x = p.x[0], &y = p.x[1];
+    // without a weight the inputs are not read, and there is no weight gradient
+    if ((x.weight != nullptr) != (dq_weight != nullptr) || (y.weight != nullptr) != (dk_weight != nullptr))
+        return GQA_ERR_INVALID_ARGUMENT;
+    if (!aligned_or_null(dq_weight, 4) || !aligned_or_null(dk_weight, 4)) return GQA_ERR_INVALID_ARGUMENT;
+    if ((x.weight && !aligned(q, 16)) || (y.weight && !aligned(k, 16))) return GQA_ERR_INVALID_ARGUMENT;
+    if ((st = check_rows(dq_out_layout, B, Hq, T, D, &x.grad_sb, &x.grad_sh, &x.grad_st)) != GQA_OK) return st;
+    if ((st = check_rows(dk_out_layout, B, Hkv, T, D, &y.grad_sb, &y.grad_sh, &y.grad_st)) != GQA_OK) return st;
+    if (x.weight && (st = check_rows(q_layout, B, Hq, T, D, &x.in_sb, &x.in_sh, &x.in_st)) != GQA_OK) return st;
+    if (y.weight && (st = check_rows(k_layout, B, Hkv, T, D, &y.in_sb, &y.in_sh, &y.in_st)) != GQA_OK) return st;
+    if ((st = check_rows(dq_layout, B, Hq, T, D, &x.out_sb, &x.out_sh, &x.out_st)) != GQA_OK) return st;
+    if ((st = check_rows(dk_layout, B, Hkv, T, D, &y.out_sb, &y.out_sh, &y.out_st)) != GQA_OK) return st;
+    const RopeBwdPlan r = rope_bwd_plan(B, T, Hq, Hkv, D);
+    if (x.weight || y.weight) {
+        if (!aligned(workspace, 256) || workspace_bytes < gqa_qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hkv, D))
+            return GQA_ERR_WORKSPACE;
+        p.partial = static_cast<float*>(workspace);
+    }
+    x.grad = static_cast<const bf16*>(dq_out);
+    y.grad = static_cast<const bf16*>(dk_out);
+    x.in = static_cast<const bf16*>(q);
+    y.in = static_cast<const bf16*>(k);
+    x.out = static_cast<bf16*>(dq);
+    y.out = static_cast<bf16*>(dk);
+    p.heads_per_team = r.heads_per_team;
+    p.blocks[0] = (Hq + r.heads_per_team - 1) / r.heads_per_team;
+    p.blocks[1] = (Hkv + r.heads_per_team - 1) / r.heads_per_team;
+    p.q_blocks = r.q_ctas;
+    const int ctas = r.q_ctas + r.k_ctas;
+    const bool inter = rope->interleaved != 0;
+    return D == 128 ? rope_bwd<128>(p, ctas, inter, dq_weight, dk_weight, static_cast<cudaStream_t>(stream))
+                    : rope_bwd<64>(p, ctas, inter, dq_weight, dk_weight, static_cast<cudaStream_t>(stream));
+}
+
+gqa_status gqa_kv4_append(const void* k, const void* v, void* k_pool, void* v_pool, const int* slots, int N, int Hkv,
+                          int D, int page_size, int num_pages, const gqa_layout* k_layout, const gqa_layout* v_layout,
+                          const gqa_kv4_layout* k_pool_layout, const gqa_kv4_layout* v_pool_layout, void* stream) {
+    return kv4_rows(true, k, v, k_pool, v_pool, slots, N, Hkv, D, page_size, num_pages, k_layout, v_layout, k_pool_layout,
+                    v_pool_layout, stream);
+}
+
+gqa_status gqa_kv4_gather(const void* k_pool, const void* v_pool, void* k, void* v, const int* slots, int N, int Hkv,
+                          int D, int page_size, int num_pages, const gqa_kv4_layout* k_pool_layout,
+                          const gqa_kv4_layout* v_pool_layout, const gqa_layout* k_layout, const gqa_layout* v_layout,
+                          void* stream) {
+    return kv4_rows(false, k, v, k_pool, v_pool, slots, N, Hkv, D, page_size, num_pages, k_layout, v_layout, k_pool_layout,
+                    v_pool_layout, stream);
+}
+
+size_t gqa_attn_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, int window) {
+    if (check_dec4(B, Hq, Hkv, Tq, max_seqlen_k, D, window) != GQA_OK) return 0;
+    const Dec4Plan r = dec4_plan(B, Hq, Hkv, Tq, max_seqlen_k, D, window);
+    return r.ctas == 1 ? 0 : dec4_bytes(r, D);
+}
+
+gqa_status gqa_attn_decode_kv4(const void* q, const void* k_pool, const void* v_pool, void* o, const int* seqlens_k,
+                               const int* block_table, int page_size, int num_pages, int max_pages, int B, int Hq,
+                               int Hkv, int Tq, int max_seqlen_k, int D, const gqa_kv4_layout* k_layout,
+                               const gqa_kv4_layout* v_layout, float softmax_scale, int window, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    gqa_status st = check_dec4(B, Hq, Hkv, Tq, max_seqlen_k, D, window);
+    if (st != GQA_OK) return st;
+    if ((st = check_pages(page_size, num_pages)) != GQA_OK) return st;
+    if (max_pages <= 0 || !aligned(q, 16) || !aligned(o, 16) || !aligned(seqlens_k, 4) || !aligned(block_table, 4))
+        return GQA_ERR_INVALID_ARGUMENT;
+    if (!std::isfinite(softmax_scale)) return GQA_ERR_INVALID_ARGUMENT;
+    gqa::Dec4Params p{};
+    if ((st = check_kv4_pool(k_pool, k_layout, num_pages, Hkv, page_size, D, &p.k_sb, &p.k_sh)) != GQA_OK) return st;
+    if ((st = check_kv4_pool(v_pool, v_layout, num_pages, Hkv, page_size, D, &p.v_sb, &p.v_sh)) != GQA_OK) return st;
+    const Dec4Plan r = dec4_plan(B, Hq, Hkv, Tq, max_seqlen_k, D, window);
+    if (r.ctas > 1) {
+        if (!aligned(workspace, 256) || workspace_bytes < dec4_bytes(r, D)) return GQA_ERR_WORKSPACE;
+        p.part = static_cast<float*>(workspace);
+        p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + dec4_lse_offset(r, D));
+    }
+    p.q = static_cast<const bf16*>(q);
+    p.o = static_cast<bf16*>(o);
+    p.k = static_cast<const uint8_t*>(k_pool);
+    p.v = static_cast<const uint8_t*>(v_pool);
+    p.seqlens = seqlens_k;
+    p.table = block_table;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.Tq = Tq;
+    p.n_rc = r.n_rc;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    p.max_pages = max_pages;
+    p.capacity = (int)std::min<long long>(max_seqlen_k, (long long)max_pages * page_size);
+    p.window = window >= max_seqlen_k ? 0 : window;  // a window covering every key is plain causal
+    p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)D)) * 1.4426950408889634f;
+    p.timeout_ns = gqa::kWaitTimeoutNs;
+    if ((p.err = gqa::device_error_ptr()) == nullptr) return GQA_ERR_CUDA;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (D == 128)
+        return r.nt == 1   ? launch_dec4<128, 1>(p, r.ctas, s)
+               : r.nt == 2 ? launch_dec4<128, 2>(p, r.ctas, s)
+                           : launch_dec4<128, 4>(p, r.ctas, s);
+    return r.nt == 1   ? launch_dec4<64, 1>(p, r.ctas, s)
+           : r.nt == 2 ? launch_dec4<64, 2>(p, r.ctas, s)
+                       : launch_dec4<64, 4>(p, r.ctas, s);
+}
+
+}  // extern "C"

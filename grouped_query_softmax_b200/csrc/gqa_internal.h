@@ -211,6 +211,9 @@ cudaError_t launch_decode(const DecLaunch& a, cudaStream_t stream);
 cudaError_t launch_bwd(const BwdLaunch& a, cudaStream_t stream);
 cudaError_t launch_selftest_wait(unsigned long long timeout_ns, cudaStream_t stream);
 
+// Address of the device error word in the current context; null if the lookup fails.
+uint32_t* device_error_ptr();
+
 // Read and clear the device error word of the current device (after a stream sync).
 cudaError_t read_and_clear_device_error(uint32_t* value);
 

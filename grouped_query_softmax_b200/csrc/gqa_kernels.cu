@@ -17,7 +17,7 @@ static_assert(kDevErrWaitTimeout == kErrBitWaitTimeout && kDevErrBadSeqlens == k
               "device and host disagree on the error bits");
 __device__ uint32_t g_device_error = 0;
 
-static uint32_t* device_error_ptr() {
+uint32_t* device_error_ptr() {
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_device_error) != cudaSuccess) return nullptr;
     return static_cast<uint32_t*>(p);

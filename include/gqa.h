@@ -404,6 +404,168 @@ GQA_API gqa_status gqa_attn_bwd(const void* q, const void* k, const void* v, con
                                 long long k_sh, long long v_sb, long long v_sh, float softmax_scale,
                                 int window, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Around the attention calls: what a paged cache needs before and after them. The pages leave
+ * these steps to the caller ("注意力家族", section Mask 与增量位置: positions come from each
+ * sequence's own lengths, not from the tensors' shapes); they run on the device here, so that a
+ * serving step is a fixed sequence of launches (one CUDA graph) whatever the lengths are.
+ *
+ * gqa_paged_plan: block tables and row numbers of one step, from request lengths.
+ * Request s holds seqlens[s] rows, keeps the first keep[s] of them (keep NULL: all) and adds
+ * new_tokens[s]; afterwards it holds seqlens_out[s] = keep[s] + new_tokens[s]. It had
+ * ceil(seqlens / page_size) pages and needs ceil(seqlens_out / page_size). free_list[0 ..
+ * free_count) is a stack of unused pool pages: the pages given back are pushed first, in the
+ * order of (request, page), then the wanted ones are popped in that order, the last pushed page
+ * first. The result does not depend on timing.
+ *   seqlens, keep, new_tokens  int32 [S]; 0 <= keep <= seqlens; S <= 8192.
+ *   block_table    int32 [S, max_pages]; entries below a request's page count are read, the
+ *                  entries of the pages it takes are written, others keep what they hold.
+ *   free_list      int32 [free_capacity]; entries at and past the new count keep what they hold.
+ *   free_count     int32 [1]; free_count_out int32 [1], may be free_count itself.
+ *   seqlens_out    int32 [S], may be seqlens itself.
+ *   cu_seqlens     int32 [S + 1]: token t of the step belongs to the request s with
+ *                  cu[s] <= t < cu[s + 1] (the cu_seqlens_q of gqa_attn_fwd_varlen_paged).
+ *   positions, slots  int32 [max_tokens], 16-byte aligned: the token's position in its request
+ *                  (keep[s] + t - cu[s]) and its cache row page * page_size + position %
+ *                  page_size (the slots of the calls below). Tokens past the last request's
+ *                  (padding of the step's batch) get position 0 and slot -1.
+ *   page_size      16, 32, 64 or a multiple of 128; num_pages the pool's pages. A table entry
+ *                  outside [0, num_pages) gives slot -1.
+ * Lengths live on the device and are checked there: if one lies outside its bounds, the tokens
+ * exceed max_tokens, or the pages run out (or would overflow free_capacity), then cache and free
+ * list stay as they are, the outputs describe an empty step (cu_seqlens 0, slots -1, seqlens_out
+ * = seqlens), and the next gqa_get_device_error() returns GQA_ERR_INVALID_ARGUMENT.
+ * Outputs must not overlap the inputs except as said above. No workspace.
+ */
+GQA_API gqa_status gqa_paged_plan(const int* seqlens, const int* keep, const int* new_tokens, int* block_table,
+                                  int* free_list, const int* free_count, int* seqlens_out, int* cu_seqlens,
+                                  int* positions, int* slots, int* free_count_out, int S, int max_pages,
+                                  int page_size, int num_pages, int free_capacity, int max_tokens, void* stream);
+
+/*
+ * RMS norm of each query and key head with the position rotation in the same pass:
+ *   n = x / sqrt(mean(x^2) + eps),  y = n * weight,  z = R(position) y,
+ * over the D elements of each row. R turns each pair (a, b) of the first `rot` elements by the
+ * angle of its position, (a c - b s, b c + a s); pairs are (i, i + rot/2), or (2i, 2i + 1) when
+ * `interleaved`. Everything between the bf16 input and the bf16 output is fp32.
+ *   q_weight, k_weight  [D] bf16, or fp32 when weight_fp32; NULL: that side is not normalised.
+ *   cos, sin       fp32 [n_positions, rot/2], contiguous, 16-byte aligned; both NULL: no rotation.
+ *   positions      int32: token t of batch b has position positions[b*positions_sb + t]; NULL: t.
+ *   rot            a multiple of 8 in [8, D].
+ * A position outside [0, n_positions) leaves its rows unwritten (backward: unwritten and without
+ * part in the weight gradients), and the next gqa_get_device_error() returns
+ * GQA_ERR_INVALID_ARGUMENT.
+ */
+typedef struct gqa_rope {
+    const void* q_weight;
+    const void* k_weight;
+    const float* cos;
+    const float* sin;
+    const int* positions;
+    long long positions_sb;
+    int n_positions, rot, interleaved, weight_fp32;
+    float eps;
+} gqa_rope;
+
+/*
+ *   q, k           bf16, rows of D in {64, 128} elements at b*sb + h*sh + t*st (gqa_layout), so
+ *                  the projection's [B, T, heads, D] output is read where it lies.
+ *   q_out, k_out   bf16, through their layouts; may be q, k themselves (same layouts).
+ */
+GQA_API gqa_status gqa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int T, int Hq,
+                                    int Hkv, int D, const gqa_layout* q_layout, const gqa_layout* k_layout,
+                                    const gqa_layout* q_out_layout, const gqa_layout* k_out_layout,
+                                    const gqa_rope* rope, void* stream);
+
+/*
+ * Backward of gqa_qk_norm_rope, given the gradients of its outputs and its inputs:
+ *   g = R^T dz,  dweight = sum over rows of g * n,  e = g * weight,
+ *   dx = (e - n mean(e * n)) / sqrt(mean(x^2) + eps).
+ *   dq_out, dk_out  bf16 gradients of q_out, k_out (for instance gqa_attn_bwd's dq and dk).
+ *   q, k            the forward's inputs; not read (may be NULL) on a side without a weight.
+ *   dq, dk          bf16; may be dq_out, dk_out themselves (same layouts).
+ *   dq_weight, dk_weight  fp32 [D], written; given exactly where the weight is.
+ *   workspace       >= gqa_qk_norm_rope_bwd_workspace_bytes(...) bytes, 256-byte aligned, when a
+ *                   weight is given; contents on entry ignored; not shared by calls that overlap.
+ * The sums run in a fixed order: the same inputs give the same bits.
+ */
+GQA_API size_t gqa_qk_norm_rope_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
+GQA_API gqa_status gqa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, void* dq,
+                                        void* dk, float* dq_weight, float* dk_weight, int B, int T, int Hq, int Hkv,
+                                        int D, const gqa_layout* dq_out_layout, const gqa_layout* dk_out_layout,
+                                        const gqa_layout* q_layout, const gqa_layout* k_layout,
+                                        const gqa_layout* dq_layout, const gqa_layout* dk_layout, const gqa_rope* rope,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Serving form of gqa_qk_norm_rope for N packed tokens: q_out gets the queries; the normalised,
+ * rotated keys and the values as they are go to row slots[t] % page_size of pool page
+ * slots[t] / page_size (gqa_paged_plan's slots). k_pool and v_pool are the bf16 pools of
+ * gqa_attn_decode_varlen and gqa_attn_fwd_varlen_paged (b = pool page, t = row of the page).
+ * A negative slot writes no row (the query is still written); a slot past the pool writes none
+ * either and is reported like a bad position. Slots of one call are distinct: of two equal ones,
+ * the row holds a mixture. N = 0 launches nothing.
+ */
+GQA_API gqa_status gqa_qk_norm_rope_append(const void* q, const void* k, const void* v, void* q_out, void* k_pool,
+                                           void* v_pool, const int* slots, int N, int Hq, int Hkv, int D,
+                                           int page_size, int num_pages, const gqa_layout* q_layout,
+                                           const gqa_layout* k_layout, const gqa_layout* v_layout,
+                                           const gqa_layout* q_out_layout, const gqa_layout* k_pool_layout,
+                                           const gqa_layout* v_pool_layout, const gqa_rope* rope, void* stream);
+
+/*
+ * A paged cache held in 4 bits: a quarter of the bf16 pool's bytes and a little over (D/2 + 4 for
+ * 2 D), so decode, which is bound by reading the cache ("注意力家族", section KV Cache 成本),
+ * reads that much less.
+ *
+ * A row of D values is D/2 + 4 bytes: element 2i in the low and 2i + 1 in the high nibble of
+ * byte i, then two bf16 values, the step s and the minimum m. It stands for s * code + m, where
+ * m is the row's smallest value, s = bf16((max - min) / 15) and code = round_half_even((x - m) *
+ * r), x - m and r = 1 / s each rounded to 32 bits: off by at most (1/2 + 15/512) s. A row with a NaN or an
+ * infinity, or whose max - min passes fp32's range, is stored as NaN; a step below 2^-126 as 0.
+ * A pool is uint8 [num_pages, Hkv, page_size, D/2 + 4] with free page and head strides.
+ */
+typedef struct gqa_kv4_layout {
+    long long sb, sh; /* bytes between pages and between heads of a page; multiples of 16 */
+} gqa_kv4_layout;
+
+/*
+ * Write rows of N tokens, k and v bf16 [N, Hkv, D] through layouts (t = token), to the rows
+ * slots[t] of the pools (as in gqa_qk_norm_rope_append), and read them back: k and v get the
+ * value rounded to bf16; a slot outside the pool reads as zeros. Pools are 16-byte aligned,
+ * page_size 16, 32, 64 or a multiple of 128. N = 0 launches nothing.
+ */
+GQA_API gqa_status gqa_kv4_append(const void* k, const void* v, void* k_pool, void* v_pool, const int* slots, int N,
+                                  int Hkv, int D, int page_size, int num_pages, const gqa_layout* k_layout,
+                                  const gqa_layout* v_layout, const gqa_kv4_layout* k_pool_layout,
+                                  const gqa_kv4_layout* v_pool_layout, void* stream);
+GQA_API gqa_status gqa_kv4_gather(const void* k_pool, const void* v_pool, void* k, void* v, const int* slots, int N,
+                                  int Hkv, int D, int page_size, int num_pages, const gqa_kv4_layout* k_pool_layout,
+                                  const gqa_kv4_layout* v_pool_layout, const gqa_layout* k_layout,
+                                  const gqa_layout* v_layout, void* stream);
+
+/*
+ * gqa_attn_decode_varlen over a cache held in 4 bits: q, o bf16 [B, Hq, Tq, D] contiguous,
+ * 1 <= Tq <= 16; sequence b's queries sit at positions L(b) - Tq .. L(b) - 1, L(b) =
+ * seqlens_k[b]; block_table int32 [B, max_pages] as there.
+ *   Scores, softmax and sums are fp32; the stored rows enter exactly, and the product of a
+ *   probability and a value row's step is rounded to bf16 (as P is in the other calls).
+ *   Every L(b) must lie in [0, min(max_seqlen_k, max_pages * page_size)], max_seqlen_k <= 2^30.
+ *   A query at a negative position (L(b) < Tq) sees no key and gets zeros. A sequence outside
+ *   that range gets no output and is reported by the next gqa_get_device_error().
+ *   Rows past L(b) may hold any bits; a page number outside [0, num_pages) reads as zeros.
+ *   window, softmax_scale  as for gqa_attn_decode_ex.
+ *   workspace  >= gqa_attn_decode_kv4_workspace_bytes(...) bytes, 256-byte aligned; may be NULL
+ *              when that is 0; contents on entry ignored; not shared by calls that overlap.
+ */
+GQA_API size_t gqa_attn_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, int window);
+GQA_API gqa_status gqa_attn_decode_kv4(const void* q, const void* k_pool, const void* v_pool, void* o,
+                                       const int* seqlens_k, const int* block_table, int page_size, int num_pages,
+                                       int max_pages, int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D,
+                                       const gqa_kv4_layout* k_layout, const gqa_kv4_layout* v_layout,
+                                       float softmax_scale, int window, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
 /* A static, human-readable name for a status code. */
 GQA_API const char* gqa_status_string(gqa_status s);
 
@@ -411,8 +573,8 @@ GQA_API const char* gqa_status_string(gqa_status s);
  * Synchronises `stream`, then reads and clears the device error word of the
  * current device. Returns GQA_ERR_TIMEOUT if a bounded wait in any kernel of this
  * library ran out since the last call, else GQA_ERR_INVALID_ARGUMENT if a
- * variable-length call found sequence bounds outside its tensors (see
- * gqa_attn_fwd_varlen, gqa_attn_decode_varlen), GQA_ERR_CUDA if the stream reports
+ * call found sequence bounds, positions or cache rows outside their tensors (see
+ * gqa_attn_fwd_varlen, gqa_attn_decode_varlen, gqa_paged_plan and the calls after it), GQA_ERR_CUDA if the stream reports
  * a CUDA error, else GQA_OK.
  */
 GQA_API gqa_status gqa_get_device_error(void* stream);
