@@ -19,7 +19,7 @@
 // different banks without padding or swizzle. P goes from its accumulator layout to the B
 // operand's with one 8x8 transpose a tile.
 //
-// Work: the tiles of 32 keys of every (sequence, KV head, row chunk) laid end to end are cut
+// Work: the tiles of 64 keys of every (sequence, KV head, row chunk) laid end to end are cut
 // into equal runs, one per CTA, so all CTAs finish together whatever the lengths. In a CTA the
 // warps take tiles in turn, each with a ring of its own that its own lanes fill with bulk
 // copies (a page's rows of one head are contiguous): no warp waits for another until the
@@ -31,9 +31,9 @@
 
 namespace gqa {
 
-constexpr int kD4Warps = 8;
-constexpr int kD4Threads = 32 * kD4Warps;
-constexpr int kD4Keys = 32;  // keys a tile
+constexpr int kD4Keys = 64;  // keys a tile: two groups of 32, the keys of two m16 tiles
+constexpr int kD4Groups = kD4Keys / 32;
+constexpr int kD4MergeThreads = 256;
 
 struct Dec4Params {
     const __nv_bfloat16* q;  // [B, Hq, Tq, D]
@@ -59,15 +59,17 @@ struct Dec4Cfg {
     static constexpr int kRow = D / 2 + 4;          // bytes of a stored row
     static constexpr int kTile = kD4Keys * kRow;    // K or V rows of a tile
     static constexpr int kStage = 2 * kTile;
-    static constexpr int kStages = NT == 4 ? 4 : 3;
+    static constexpr int kStages = 2;
+    static constexpr int kWarps = NT == 4 ? 8 : 6;
+    static constexpr int kThreads = 32 * kWarps;
     static constexpr int kCtasPerSm = NT == 4 ? 1 : 2;
     static constexpr int kWarpBytes = kStages * kStage;
-    static constexpr int kQOff = kD4Warps * kWarpBytes;
+    static constexpr int kQOff = kWarps * kWarpBytes;
     static constexpr int kQBytes = NT == 1 ? 0 : (D / 32) * NT * 32 * 16;  // Q fragments
     static constexpr int kCtlOff = kQOff + kQBytes;
     struct Ctl {
-        uint64_t full[kD4Warps][kStages];
-        unsigned long long sums[kD4Warps];
+        uint64_t full[kWarps][kStages];
+        unsigned long long sums[kWarps];
         unsigned long long first;  // work before the sequence that holds this CTA's first tile
         int b;                     // that sequence
         uint32_t abort;
@@ -98,12 +100,23 @@ __device__ __forceinline__ unsigned long long dec4_cut(unsigned long long total,
     return total * i / ctas;  // total is below 2^52 (checked on the host), i a few hundred
 }
 
-// Two codes as bf16 numbers 16 + c: nibble e of the low half and of the high half.
-template <int e>
-__device__ __forceinline__ uint32_t dec4_codes(uint32_t w) {
-    const uint32_t x = e == 0 ? w << 3 : w >> (4 * e - 3);
-    return (x & 0x00780078u) | 0x41804180u;
-}
+// Two codes as bf16 numbers 16 + c: nibble e of the low half and of the high half. The constants
+// come in registers that the compiler cannot see through: a logic operation takes one immediate
+// only, and it would spend two on them.
+struct Dec4Bits {
+    uint32_t mask, base;
+    __device__ __forceinline__ Dec4Bits() {
+        asm volatile("mov.b32 %0, 0x00780078;" : "=r"(mask));
+        asm volatile("mov.b32 %0, 0x41804180;" : "=r"(base));
+    }
+    template <int e>
+    __device__ __forceinline__ uint32_t codes(uint32_t w) const {
+        const uint32_t x = e == 0 ? w << 3 : w >> (4 * e - 3);
+        uint32_t d;
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "r"(mask), "r"(base));  // (x & mask) | base
+        return d;
+    }
+};
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -136,9 +149,11 @@ __device__ __forceinline__ void dec4_sums(int B, int upto, unsigned long long* w
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kD4Threads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_decode_kv4_kernel(const Dec4Params p) {
+__global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_decode_kv4_kernel(const Dec4Params p) {
     using C = Dec4Cfg<D, NT>;
     constexpr int kStages = C::kStages;
+    constexpr int kWarps = C::kWarps;
+    constexpr int U = kD4Groups;
     constexpr int RW = C::kRow / 4;  // words of a stored row
     constexpr int kKI = D / 32;      // word groups of a key row: four words, one a lane of a quad
     constexpr int kVI = D / 64;      // word groups of a value row: eight words, one a quad
@@ -160,17 +175,17 @@ __global__ void __launch_bounds__(kD4Threads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_de
     const int units = p.Hkv * p.n_rc;  // units of a sequence
     const auto work_of = [&](int b) { return (unsigned long long)dec4_seq(p, b).n * units; };
     unsigned long long total, before;
-    dec4_sums<kD4Warps>(p.B, 0, ctl->sums, work_of, &before, &total);
+    dec4_sums<kWarps>(p.B, 0, ctl->sums, work_of, &before, &total);
     const unsigned ctas = (unsigned)min((unsigned long long)gridDim.x, total);
     if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < p.B; b += kD4Threads)
+        for (int b = threadIdx.x; b < p.B; b += C::kThreads)
             if (dec4_seq(p, b).n == 0) atomicOr(p.err, kDevErrBadSeqlens);
     if (blockIdx.x >= ctas) return;
     unsigned long long at = dec4_cut(total, blockIdx.x, ctas);
     const unsigned long long end = dec4_cut(total, blockIdx.x + 1, ctas);
     {
         unsigned long long run = 0;  // work before this round's sequences
-        for (int b0 = 0; b0 < p.B && run <= at; b0 += kD4Threads) {
+        for (int b0 = 0; b0 < p.B && run <= at; b0 += C::kThreads) {
             const int b = b0 + threadIdx.x;
             const unsigned long long x = b < p.B ? work_of(b) : 0;
             unsigned long long inc = x;
@@ -188,7 +203,7 @@ __global__ void __launch_bounds__(kD4Threads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_de
                 ctl->b = b;
                 ctl->first = lo;
             }
-            for (int w = 0; w < kD4Warps; ++w) run += ctl->sums[w];
+            for (int w = 0; w < kWarps; ++w) run += ctl->sums[w];
             __syncthreads();
         }
     }
@@ -197,8 +212,10 @@ __global__ void __launch_bounds__(kD4Threads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_de
     Dec4Seq s = dec4_seq(p, b);
 
     const float sl2 = p.scale_log2;
+    const Dec4Bits bits;
     const int box = min(p.page_size, kD4Keys);  // rows of one bulk copy
-    const int boxes = kD4Keys / box;            // 1, or 2 for pages of 16 rows
+    const int boxes = kD4Keys / box;
+    const int page_step = kWarps * kD4Keys / p.page_size, row_step = kWarps * kD4Keys - page_step * p.page_size;
     volatile uint32_t* abort_flag = &ctl->abort;
     int stage = 0;
     uint32_t phase = 0;
@@ -219,30 +236,30 @@ __global__ void __launch_bounds__(kD4Threads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_de
         const int nrows = min(C::kRows, p.G * p.Tq - rbase);
         const size_t row0 = ((size_t)b * p.Hq + (size_t)h * p.G) * p.Tq + rbase;
         const int key_base = (s.first + t0) * kD4Keys;
-        const int n_mine = (t1 - t0 - warp + kD4Warps - 1) / kD4Warps;  // tiles warp, warp + kD4Warps, ...
+        const int n_mine = (t1 - t0 - warp + kWarps - 1) / kWarps;  // tiles warp, warp + kWarps, ...
         const uint8_t* k_head = p.k + h * p.k_sh;
         const uint8_t* v_head = p.v + h * p.v_sh;
 
-        // Pool page of this lane's box of the warp's tile i.
-        const auto look_up = [&](int i) {
-            const int key = key_base + (warp + i * kD4Warps) * kD4Keys + lane * box;
-            return i < n_mine && lane < boxes && key < s.len ? __ldg(p.table + (size_t)b * p.max_pages + key / p.page_size)
-                                                             : -1;
-        };
-        // Copy the warp's tile i into ring stage st. Boxes past the sequence are left out (their
-        // keys are masked); a page number outside the pool reads as rows of zeros.
-        const auto fetch = [&](int i, int st, int page) {
-            const int key = key_base + (warp + i * kD4Warps) * kD4Keys + lane * box;
-            const bool want = lane < boxes && key < s.len;
-            const bool ok = want && page >= 0 && page < p.num_pages;
+        // The next tile to fetch: this lane's box starts at key next_key, row next_row of pool page
+        // next_page (-1: none), which is looked up one tile ahead of its copy.
+        int next_key = key_base + warp * kD4Keys + lane * box;
+        int ord = next_key / p.page_size, next_row = next_key - ord * p.page_size;
+        const int* table = p.table + (size_t)b * p.max_pages;
+        const auto look_up = [&]() { return lane < boxes && next_key < s.len ? __ldg(table + ord) : -1; };
+        int next_page = look_up();
+        // Copy the next tile into ring stage st. Boxes past the sequence are left out (their keys
+        // are masked); a page number outside the pool reads as rows of zeros.
+        const auto fetch = [&](int st) {
+            const bool want = lane < boxes && next_key < s.len;
+            const bool ok = want && (unsigned)next_page < (unsigned)p.num_pages;
             const unsigned oks = __ballot_sync(0xffffffffu, ok), wants = __ballot_sync(0xffffffffu, want);
             const uint32_t bar = bars + 8 * st, dst = ring_addr + st * C::kStage + lane * box * C::kRow;
             if (lane == 0) mbar_arrive_expect_tx(bar, __popc(oks) * 2 * box * C::kRow);
             __syncwarp();
             if (ok) {
-                const long long row = (long long)(key % p.page_size) * C::kRow;
-                bulk_load(dst, k_head + page * p.k_sb + row, box * C::kRow, bar);
-                bulk_load(dst + C::kTile, v_head + page * p.v_sb + row, box * C::kRow, bar);
+                const long long row = (long long)next_row * C::kRow;
+                bulk_load(dst, k_head + next_page * p.k_sb + row, box * C::kRow, bar);
+                bulk_load(dst + C::kTile, v_head + next_page * p.v_sb + row, box * C::kRow, bar);
             }
             if (oks != wants) {
                 for (int x = 0; x < boxes; ++x)
@@ -253,11 +270,17 @@ __global__ void __launch_bounds__(kD4Threads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_de
                         }
                 fence_proxy_async_smem();  // before a later copy into these bytes
             }
+            next_key += kWarps * kD4Keys;
+            ord += page_step;
+            next_row += row_step;
+            if (next_row >= p.page_size) {
+                next_row -= p.page_size;
+                ++ord;
+            }
+            next_page = look_up();
         };
-        int page = look_up(0);
         for (int i = 0, st = stage; i < kStages && i < n_mine; ++i) {
-            fetch(i, st, page);
-            page = look_up(i + 1);
+            fetch(st);
             st = st + 1 == kStages ? 0 : st + 1;
         }
 
@@ -323,16 +346,19 @@ __global__ void __launch_bounds__(kD4Threads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_de
             }
             const uint32_t* K = reinterpret_cast<const uint32_t*>(ring + stage * C::kStage);
             const uint32_t* V = K + C::kTile / 4;
-            const int key0 = key_base + (warp + it * kD4Warps) * kD4Keys;
-            // ---- S^T = K Q^T: accumulator rows g, g + 8 are keys 4g + 2mt, 4g + 2mt + 1
-            float sacc[2][NT][4];
+            const int key0 = key_base + (warp + it * kWarps) * kD4Keys;
+            // ---- S^T = K Q^T: of each group of 32 keys, accumulator rows g, g + 8 of m16 tile mt are
+            // keys 4g + 2mt, 4g + 2mt + 1
+            float sacc[U][2][NT][4];
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int j = 0; j < U; ++j)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    sacc[mt][nt][0] = sacc[mt][nt][2] = -16.f * sumq[nt][0];
-                    sacc[mt][nt][1] = sacc[mt][nt][3] = -16.f * sumq[nt][1];
-                }
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        sacc[j][mt][nt][0] = sacc[j][mt][nt][2] = -16.f * sumq[nt][0];
+                        sacc[j][mt][nt][1] = sacc[j][mt][nt][3] = -16.f * sumq[nt][1];
+                    }
             const uint32_t* kr = K + 4 * g * RW + t;
 #pragma unroll
             for (int i = 0; i < kKI; ++i) {
@@ -345,27 +371,49 @@ __global__ void __launch_bounds__(kD4Threads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_de
                         f[nt] = reinterpret_cast<const uint4*>(dec4_smem + C::kQOff)[(i * NT + nt) * 32 + lane];
                 }
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
-                    const uint32_t w0 = kr[(2 * mt) * RW + 4 * i], w1 = kr[(2 * mt + 1) * RW + 4 * i];
-                    const uint32_t a[4] = {dec4_codes<0>(w0), dec4_codes<0>(w1), dec4_codes<1>(w0), dec4_codes<1>(w1)};
-                    const uint32_t c[4] = {dec4_codes<2>(w0), dec4_codes<2>(w1), dec4_codes<3>(w0), dec4_codes<3>(w1)};
+                for (int j = 0; j < U; ++j)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_bf16_16816(sacc[mt][nt], a, f[nt].x, f[nt].y);
-                        mma_bf16_16816(sacc[mt][nt], c, f[nt].z, f[nt].w);
+                    for (int mt = 0; mt < 2; ++mt) {
+                        const uint32_t* w = kr + (32 * j + 2 * mt) * RW + 4 * i;
+                        const uint32_t w0 = w[0], w1 = w[RW];
+                        const uint32_t a[4] = {bits.template codes<0>(w0), bits.template codes<0>(w1), bits.template codes<1>(w0), bits.template codes<1>(w1)};
+                        const uint32_t c[4] = {bits.template codes<2>(w0), bits.template codes<2>(w1), bits.template codes<3>(w0), bits.template codes<3>(w1)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_bf16_16816(sacc[j][mt][nt], a, f[nt].x, f[nt].y);
+                            mma_bf16_16816(sacc[j][mt][nt], c, f[nt].z, f[nt].w);
+                        }
                     }
-                }
             }
-            // ---- scores in log2 units
-            const bool masked = key0 + kD4Keys > pos_min + 1 || key0 < lo_max;
-            float kscale[4], kmin[4], vscale[4], vmid[4];
+            // ---- scores in log2 units; score(j, c, nt, x) is of key 32j + 4g + c, row 8nt + 2t + x
+            const auto score = [&](int j, int c, int nt, int x) -> float& { return sacc[j][c >> 1][nt][(c & 1) * 2 + x]; };
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t kh = K[(4 * g + c) * RW + D / 8], vh = V[(4 * g + c) * RW + D / 8];
-                kscale[c] = __uint_as_float(kh << 16) * sl2;
-                kmin[c] = __uint_as_float(kh & 0xffff0000u) * sl2;
-                vscale[c] = __uint_as_float(vh << 16);
-                vmid[c] = fmaf(8.f, vscale[c], __uint_as_float(vh & 0xffff0000u));
+            for (int j = 0; j < U; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t head = K[(32 * j + 4 * g + c) * RW + D / 8];
+                    const float step = __uint_as_float(head << 16) * sl2, least = __uint_as_float(head & 0xffff0000u) * sl2;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            score(j, c, nt, x) = fmaf(score(j, c, nt, x), step, least * sumq[nt][x]);
+                }
+            const bool masked = key0 + kD4Keys > pos_min + 1 || key0 < lo_max;
+            if (masked) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        // keys this row sees, counted from 4g of the tile
+                        const int hi = pos_min + (rbase + 8 * nt + 2 * t + x) % p.Tq - key0 - 4 * g;
+                        const int lo = p.window > 0 ? hi - p.window + 1 : -0x40000000;
+#pragma unroll
+                        for (int j = 0; j < U; ++j)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                if (32 * j + c > hi || 32 * j + c < lo) score(j, c, nt, x) = -INFINITY;
+                    }
             }
             bool raise = false;
             float m_new[NT][2];
@@ -373,24 +421,14 @@ __global__ void __launch_bounds__(kD4Threads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_de
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    int hi = 0x7fffffff, lo = -1;  // keys this row sees, in the tile's numbering
-                    if (masked) {
-                        const int pos = s.len - p.Tq + (rbase + 8 * nt + 2 * t + x) % p.Tq;
-                        hi = pos - key0;
-                        lo = p.window > 0 ? hi - p.window + 1 : -1;
-                    }
                     float mx = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float& sc = sacc[c >> 1][nt][(c & 1) * 2 + x];
-                        sc = fmaf(sc, kscale[c], kmin[c] * sumq[nt][x]);
-                        if (masked && (4 * g + c > hi || 4 * g + c < lo)) sc = -INFINITY;
-                        mx = fmaxf(mx, sc);
-                    }
+                    for (int j = 0; j < U; ++j)
+#pragma unroll
+                        for (int c = 0; c < 4; c += 2) mx = max3f(mx, score(j, c, nt, x), score(j, c + 1, nt, x));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    m_new[nt][x] = fmaxf(m[nt][x], mx);
+                    m_new[nt][x] = max3f(mx, __shfl_xor_sync(0xffffffffu, mx, 16), m[nt][x]);
                     raise |= m_new[nt][x] > m[nt][x];
                 }
             if (__any_sync(0xffffffffu, raise)) {
@@ -410,48 +448,61 @@ __global__ void __launch_bounds__(kD4Threads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_de
                         }
                     }
             }
-            uint32_t pb[NT][4];  // B operand: keys 8t + c and 8t + 4 + c of query row g
+            float neg_m[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float w[2];
+                for (int x = 0; x < 2; ++x) neg_m[nt][x] = m[nt][x] == -INFINITY ? 0.f : -m[nt][x];
+            uint32_t pb[U][NT][4];  // B operand: keys 8t + c and 8t + 4 + c of query row g
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float sc = sacc[c >> 1][nt][(c & 1) * 2 + x];
-                        const float mu = m[nt][x] == -INFINITY ? 0.f : m[nt][x];
-                        const float e = ex2_approx(sc - mu);
-                        l[nt][x] += e;
-                        w[x] = e * vscale[c];
-                        float y = e * vmid[c];
-                        if (masked && sc == -INFINITY) w[x] = y = 0.f;  // such a key's scale may be NaN
-                        beta[nt][x] += y;
+            for (int j = 0; j < U; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t head = V[(32 * j + 4 * g + c) * RW + D / 8];
+                    const float step = __uint_as_float(head << 16);
+                    const float mid = fmaf(8.f, step, __uint_as_float(head & 0xffff0000u));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float w[2];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float sc = score(j, c, nt, x);
+                            const float e = ex2_approx(sc + neg_m[nt][x]);
+                            l[nt][x] += e;
+                            if (masked && sc == -INFINITY) {  // such a key's step may be NaN
+                                w[x] = 0.f;
+                            } else {
+                                w[x] = e * step;
+                                beta[nt][x] = fmaf(e, mid, beta[nt][x]);
+                            }
+                        }
+                        pb[j][nt][c] = movmatrix_trans(pack_bf16x2(w[0], w[1]));
                     }
-                    pb[nt][c] = movmatrix_trans(pack_bf16x2(w[0], w[1]));
                 }
             // ---- O^T += V^T P^T
             const uint32_t* vr = V + 8 * t * RW + g;
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
+            for (int ks = 0; ks < 2 * U; ++ks) {  // 16 keys: sets c0, c0 + 1 of group ks / 2
+                const int c0 = ks % 2 * 2;
                 uint32_t lo[2][kVI], hi[2][kVI];
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int i = 0; i < kVI; ++i) {
-                        const uint32_t x = vr[(2 * ks + c) * RW + 8 * i], y = vr[(2 * ks + c + 4) * RW + 8 * i];
-                        lo[c][i] = __byte_perm(x, y, 0x5410);
-                        hi[c][i] = __byte_perm(x, y, 0x7632);
+                        const uint32_t* w = vr + (32 * (ks / 2) + c0 + c) * RW + 8 * i;
+                        lo[c][i] = __byte_perm(w[0], w[4 * RW], 0x5410);
+                        hi[c][i] = __byte_perm(w[0], w[4 * RW], 0x7632);
                     }
                 const auto product = [&](float (&acc)[NT][4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
                     const uint32_t a[4] = {a0, a1, a2, a3};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(acc[nt], a, pb[nt][2 * ks], pb[nt][2 * ks + 1]);
+                    for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(acc[nt], a, pb[ks / 2][nt][c0], pb[ks / 2][nt][c0 + 1]);
                 };
                 constexpr uint32_t kOne = 0x3F803F80u;
                 product(ones, kOne, kOne, kOne, kOne);
                 if constexpr (D == 128) {  // rows g, g + 8 of tile e: d = 8g + e, 64 + 8g + e
 #define GQA_D4_HALF(x, e, tile) \
-    product(oacc[tile], dec4_codes<e>(x[0][0]), dec4_codes<e>(x[0][1]), dec4_codes<e>(x[1][0]), dec4_codes<e>(x[1][1]))
+    product(oacc[tile], bits.template codes<e>(x[0][0]), bits.template codes<e>(x[0][1]), bits.template codes<e>(x[1][0]), bits.template codes<e>(x[1][1]))
                     GQA_D4_HALF(lo, 0, 0);
                     GQA_D4_HALF(lo, 1, 1);
                     GQA_D4_HALF(lo, 2, 2);
@@ -463,7 +514,7 @@ __global__ void __launch_bounds__(kD4Threads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_de
 #undef GQA_D4_HALF
                 } else {  // rows g, g + 8 of tile e: d = 8g + e, 8g + 4 + e
 #define GQA_D4_ALL(e) \
-    product(oacc[e], dec4_codes<e>(lo[0][0]), dec4_codes<e>(hi[0][0]), dec4_codes<e>(lo[1][0]), dec4_codes<e>(hi[1][0]))
+    product(oacc[e], bits.template codes<e>(lo[0][0]), bits.template codes<e>(hi[0][0]), bits.template codes<e>(lo[1][0]), bits.template codes<e>(hi[1][0]))
                     GQA_D4_ALL(0);
                     GQA_D4_ALL(1);
                     GQA_D4_ALL(2);
@@ -472,10 +523,7 @@ __global__ void __launch_bounds__(kD4Threads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_de
                 }
             }
             __syncwarp();  // every lane has read the stage
-            if (it + kStages < n_mine) {
-                fetch(it + kStages, stage, page);
-                page = look_up(it + kStages + 1);
-            }
+            if (it + kStages < n_mine) fetch(stage);
             if (++stage == kStages) {
                 stage = 0;
                 phase ^= 1u;
@@ -510,17 +558,17 @@ __global__ void __launch_bounds__(kD4Threads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_de
         if (*abort_flag) return;  // uniform: the flag is set before the barrier and never cleared
         const bool whole = t0 == 0 && t1 == s.n;
         const size_t slot = 2 * (size_t)blockIdx.x + (t0 > 0 ? 0 : 1);
-        for (int idx = threadIdx.x; idx < nrows * D; idx += kD4Threads) {
+        for (int idx = threadIdx.x; idx < nrows * D; idx += C::kThreads) {
             const int row = idx / D, d = idx - row * D;
             constexpr int kStep = C::kWarpBytes / 4;
             const float* base = reinterpret_cast<const float*>(dec4_smem);
             float M = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kD4Warps; ++w) M = fmaxf(M, base[w * kStep + row]);
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, base[w * kStep + row]);
             const float mu = M == -INFINITY ? 0.f : M;
             float sum = 0.f, acc = 0.f;
 #pragma unroll
-            for (int w = 0; w < kD4Warps; ++w) {
+            for (int w = 0; w < kWarps; ++w) {
                 const float f = ex2_approx(base[w * kStep + row] - mu);
                 sum += base[w * kStep + C::kRows + row] * f;
                 acc += base[w * kStep + 2 * C::kRows + row * D + d] * f;
@@ -542,14 +590,15 @@ __global__ void __launch_bounds__(kD4Threads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_de
 // Merge the pieces of the units that were cut between CTAs, in CTA order: one block a unit, one
 // warp a row. The cuts are computed again from the lengths.
 template <int D, int NT>
-__global__ void __launch_bounds__(kD4Threads) gqa_decode_kv4_merge_kernel(const Dec4Params p, unsigned grid) {
+__global__ void __launch_bounds__(kD4MergeThreads) gqa_decode_kv4_merge_kernel(const Dec4Params p, unsigned grid) {
     constexpr int kRows = 8 * NT;
     constexpr int E = D / 32;
-    __shared__ unsigned long long sums[kD4Warps];
+    constexpr int kWarps = kD4MergeThreads / 32;
+    __shared__ unsigned long long sums[kWarps];
     const int units = p.Hkv * p.n_rc;
     const int b = blockIdx.x / units, u = blockIdx.x - b * units;
     unsigned long long total, before;
-    dec4_sums<kD4Warps>(
+    dec4_sums<kWarps>(
         p.B, b, sums, [&](int i) { return (unsigned long long)dec4_seq(p, i).n * units; }, &before, &total);
     const int n = dec4_seq(p, b).n;
     if (n == 0) return;
@@ -561,7 +610,7 @@ __global__ void __launch_bounds__(kD4Threads) gqa_decode_kv4_merge_kernel(const 
     const int h = u / p.n_rc, rbase = (u - h * p.n_rc) * kRows;
     const int nrows = min(kRows, p.G * p.Tq - rbase);
     const int lane = threadIdx.x & 31;
-    for (int row = threadIdx.x >> 5; row < nrows; row += kD4Warps) {
+    for (int row = threadIdx.x >> 5; row < nrows; row += kWarps) {
         // the first piece starts the unit (slot 1 of its CTA), the others do not (slot 0)
         const auto at = [&](unsigned c) { return (2 * (size_t)c + (c == c0 ? 1 : 0)) * kRows + row; };
         float M = -INFINITY;

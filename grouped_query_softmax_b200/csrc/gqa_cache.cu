@@ -231,11 +231,11 @@ Dec4Plan dec4_plan(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, int 
     const int rows = Hq / Hkv * Tq;
     r.nt = dec4_nt(rows);
     r.n_rc = (rows + 8 * r.nt - 1) / (8 * r.nt);
-    const int per_sm = r.nt == 4 ? 1 : 2;
+    const int per_sm = r.nt == 4 ? 1 : 2, warps = r.nt == 4 ? 8 : 6;  // as Dec4Cfg
     // no more CTAs than the longest lengths would give a tile for each warp
     const long long keys = window > 0 ? std::min<long long>(max_seqlen_k, (long long)window + Tq + gqa::kD4Keys) : max_seqlen_k;
     const long long tiles = (keys + gqa::kD4Keys - 1) / gqa::kD4Keys;
-    const long long most = ((long long)B * Hkv * r.n_rc * tiles + gqa::kD4Warps - 1) / gqa::kD4Warps;
+    const long long most = ((long long)B * Hkv * r.n_rc * tiles + warps - 1) / warps;
     r.ctas = (int)std::min<long long>((long long)sm_count() * per_sm, most);
     return r;
 }
@@ -250,10 +250,10 @@ gqa_status launch_dec4(const gqa::Dec4Params& p, int ctas, cudaStream_t stream) 
     cudaError_t e = cudaFuncSetAttribute(gqa::gqa_decode_kv4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::kBytes);
     if (e != cudaSuccess) return GQA_ERR_CUDA;
-    gqa::gqa_decode_kv4_kernel<D, NT><<<(unsigned)ctas, gqa::kD4Threads, C::kBytes, stream>>>(p);
+    gqa::gqa_decode_kv4_kernel<D, NT><<<(unsigned)ctas, C::kThreads, C::kBytes, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess || ctas == 1) return launched(e);
     gqa::gqa_decode_kv4_merge_kernel<D, NT>
-        <<<(unsigned)(p.B * p.Hkv * p.n_rc), gqa::kD4Threads, 0, stream>>>(p, (unsigned)ctas);
+        <<<(unsigned)(p.B * p.Hkv * p.n_rc), gqa::kD4MergeThreads, 0, stream>>>(p, (unsigned)ctas);
     return launched(cudaGetLastError());
 }
 
