@@ -1,15 +1,15 @@
 // Decode over a paged cache held in 4 bits (rows as kv4_rows_sm100.cuh writes them): up to 16
 // new queries a sequence, any group size, optional sliding window.
 //
-// A stored row is k_j = s_j c_j + m_j with codes c in 0..15, so with the 16 added to every code
-// by the bit pattern below
-//   q . k_j = s_j (q . (16 + c_j) - 16 sum(q)) + m_j sum(q),
-//   sum_j p_j v_j = sum_j w_j (16 + c_j) - 24 sum_j w_j + sum_j p_j (m_j + 8 s_j),  w_j = bf16(p_j s_j).
-// A code becomes a bf16 number with one shift and one logic operation for two of them (16 + c is
-// the bits 0x4180 | c << 3, exact), the scales stay out of the products, and the products run on
-// tensor cores in bf16 with fp32 sums. w is the only rounding besides the output's: it is taken
-// about the middle of the code range (8), so it costs what rounding P to bf16 costs. A row's NaN
-// can only reach the queries that see the key: the codes themselves are always finite.
+// A stored row is k_j = s_j c_j + m_j with codes c in 0..15. With the offset z that unpacking adds
+// to a code,
+//   q . k_j = s_j (q . (z + c_j) - z . q) + m_j sum(q),
+//   sum_j p_j v_j = sum_j w_j (16 + c_j) - 24 sum_j w_j + sum_j p_j (m_j + 8 s_j),  w_j = bf16(p_j s_j):
+// the scales stay out of the products, which run on tensor cores with fp32 sums. K's products
+// are fp16 (codes and q fit it exactly, see below), V's bf16 (w needs the range). w is the only
+// rounding besides the output's: it is taken about the middle of the code range (8), so it
+// costs what rounding P to bf16 costs. A row's NaN can only reach the queries that see the key:
+// the codes themselves are always finite.
 //
 // Keys are the M dimension of the products and query rows their N (8 a tile), so that one
 // unpacked fragment serves every query row of the KV head. mma m16n8k16 takes any order of the
@@ -26,6 +26,8 @@
 // piece ends. A unit cut between CTAs leaves fp32 partials that a second kernel merges in
 // a fixed order. Bound by HBM: D + 8 bytes a key and KV head.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "sm100_ptx.cuh"
 
@@ -100,23 +102,52 @@ __device__ __forceinline__ unsigned long long dec4_cut(unsigned long long total,
     return total * i / ctas;  // total is below 2^52 (checked on the host), i a few hundred
 }
 
-// Two codes as bf16 numbers 16 + c: nibble e of the low half and of the high half. The constants
-// come in registers that the compiler cannot see through: a logic operation takes one immediate
-// only, and it would spend two on them.
+// Pairs of codes, nibble e of a word's low half and of its high half, as numbers offset + c: one
+// shift and one logic operation in bf16 (16 + c is the bits 0x4180 | c << 3), one and a half in
+// fp16, whose ten mantissa bits hold two nibbles (256 + c at bits 2-5, 16 + c at bits 6-9). The
+// constants come in registers that the compiler cannot see through: a logic operation takes one
+// immediate only, and it would spend two on them; and the left shifts are products, which leave
+// the pipe of the shifts and logic operations, the kernel's busiest, to the others.
 struct Dec4Bits {
-    uint32_t mask, base;
+    uint32_t mask, base, mask_even, base_even, mask_odd, base_odd, four, eight;
     __device__ __forceinline__ Dec4Bits() {
         asm volatile("mov.b32 %0, 0x00780078;" : "=r"(mask));
         asm volatile("mov.b32 %0, 0x41804180;" : "=r"(base));
+        asm volatile("mov.b32 %0, 0x003C003C;" : "=r"(mask_even));
+        asm volatile("mov.b32 %0, 0x5C005C00;" : "=r"(base_even));
+        asm volatile("mov.b32 %0, 0x03C003C0;" : "=r"(mask_odd));
+        asm volatile("mov.b32 %0, 0x4C004C00;" : "=r"(base_odd));
+        asm volatile("mov.b32 %0, 4;" : "=r"(four));
+        asm volatile("mov.b32 %0, 8;" : "=r"(eight));
     }
-    template <int e>
-    __device__ __forceinline__ uint32_t codes(uint32_t w) const {
-        const uint32_t x = e == 0 ? w << 3 : w >> (4 * e - 3);
+    static __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t o) {
         uint32_t d;
-        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "r"(mask), "r"(base));  // (x & mask) | base
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "r"(m), "r"(o));  // (x & m) | o
         return d;
     }
+    // bf16 16 + c
+    template <int e>
+    __device__ __forceinline__ uint32_t codes(uint32_t w) const {
+        return and_or(e == 0 ? w * eight : w >> (4 * e - 3), mask, base);
+    }
+    // fp16: 256 + c of nibbles 0 and 2, 16 + c of nibbles 1 and 3
+    __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&d)[4]) const {
+        const uint32_t lo = w * four, hi = w >> 6;
+        d[0] = and_or(lo, mask_even, base_even);
+        d[1] = and_or(lo, mask_odd, base_odd);
+        d[2] = and_or(hi, mask_even, base_even);
+        d[3] = and_or(hi, mask_odd, base_odd);
+    }
 };
+// D = A(16x16 fp16, row) * B(16x8 fp16, col) + C, fp32 accumulate.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -211,7 +242,6 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
     unsigned long long seq0 = ctl->first;
     Dec4Seq s = dec4_seq(p, b);
 
-    const float sl2 = p.scale_log2;
     const Dec4Bits bits;
     const int box = min(p.page_size, kD4Keys);  // rows of one bulk copy
     const int boxes = kD4Keys / box;
@@ -284,12 +314,17 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
             st = st + 1 == kStages ? 0 : st + 1;
         }
 
-        // ---- Q fragments: lane (g, t) holds words t + 4i of row g's elements, as pairs (e, e + 4)
+        // ---- Q fragments: lane (g, t) holds words t + 4i of row g's elements, as pairs (e, e + 4).
+        // They are fp16, each row times the power of two that takes its largest element to [2^7, 2^8):
+        // exact (fp16 has three bits more) down to 2^-24 of the largest, and off by at most 2^-33 of
+        // it below. A row with an infinity or a NaN keeps it, and zeros stay zeros.
         uint4 qf[NT == 1 ? kKI : 1];
-        float sumq[NT][2];  // sums of the rows 2t, 2t + 1 of each tile
+        // of the rows 2t, 2t + 1 of each tile, in the scaled units: the sum, the sum times the codes'
+        // offsets, and the factor back to log2 units
+        float sumq[NT][2], offq[NT][2], unit[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float sum = 0.f;
+            float f[kKI][8], top = 0.f;
             const bool row_ok = 8 * nt + g < nrows;
 #pragma unroll
             for (int i = 0; i < kKI; ++i) {
@@ -297,19 +332,49 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                 if (row_ok) x = *reinterpret_cast<const uint4*>(p.q + (row0 + 8 * nt + g) * D + 8 * (t + 4 * i));
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    sum += __uint_as_float(w[e] << 16) + __uint_as_float(w[e] & 0xffff0000u);
-                const uint4 f = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                                           __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-                if constexpr (NT == 1)
-                    qf[i] = f;
-                else if (warp == 0)
-                    reinterpret_cast<uint4*>(dec4_smem + C::kQOff)[(i * NT + nt) * 32 + lane] = f;
+                for (int e = 0; e < 4; ++e) {
+                    f[i][2 * e] = __uint_as_float(w[e] << 16);
+                    f[i][2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[i][e]));
             }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            sumq[nt][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
-            sumq[nt][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // exponents of the factor and its inverse, both of normal numbers
+            const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 254);
+            const float up = __uint_as_float((uint32_t)(261 - ex) << 23), down = __uint_as_float((uint32_t)(ex - 7) << 23);
+            float sum = 0.f, even = 0.f;
+#pragma unroll
+            for (int i = 0; i < kKI; ++i) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    f[i][e] *= up;
+                    sum += f[i][e];
+                    if (e % 2 == 0) even += f[i][e];
+                }
+                const auto pair = [&](int e) {
+                    const __half2 h = __floats2half2_rn(f[i][e], f[i][e + 4]);
+                    return *reinterpret_cast<const uint32_t*>(&h);
+                };
+                const uint4 v = make_uint4(pair(0), pair(1), pair(2), pair(3));
+                if constexpr (NT == 1)
+                    qf[i] = v;
+                else if (warp == 0)
+                    reinterpret_cast<uint4*>(dec4_smem + C::kQOff)[(i * NT + nt) * 32 + lane] = v;
+            }
+            float off = fmaf(240.f, even, 16.f * sum);
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                off += __shfl_xor_sync(0xffffffffu, off, d);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                sumq[nt][x] = __shfl_sync(0xffffffffu, sum, 8 * t + 4 * x);
+                offq[nt][x] = -__shfl_sync(0xffffffffu, off, 8 * t + 4 * x);
+                unit[nt][x] = __shfl_sync(0xffffffffu, down, 8 * t + 4 * x) * p.scale_log2;
+            }
         }
         if constexpr (NT > 1) __syncthreads();
 
@@ -356,8 +421,8 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                 for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        sacc[j][mt][nt][0] = sacc[j][mt][nt][2] = -16.f * sumq[nt][0];
-                        sacc[j][mt][nt][1] = sacc[j][mt][nt][3] = -16.f * sumq[nt][1];
+                        sacc[j][mt][nt][0] = sacc[j][mt][nt][2] = offq[nt][0];
+                        sacc[j][mt][nt][1] = sacc[j][mt][nt][3] = offq[nt][1];
                     }
             const uint32_t* kr = K + 4 * g * RW + t;
 #pragma unroll
@@ -375,24 +440,24 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt) {
                         const uint32_t* w = kr + (32 * j + 2 * mt) * RW + 4 * i;
-                        const uint32_t w0 = w[0], w1 = w[RW];
-                        const uint32_t a[4] = {bits.template codes<0>(w0), bits.template codes<0>(w1), bits.template codes<1>(w0), bits.template codes<1>(w1)};
-                        const uint32_t c[4] = {bits.template codes<2>(w0), bits.template codes<2>(w1), bits.template codes<3>(w0), bits.template codes<3>(w1)};
+                        uint32_t a0[4], a1[4];
+                        bits.codes_f16(w[0], a0);
+                        bits.codes_f16(w[RW], a1);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma_bf16_16816(sacc[j][mt][nt], a, f[nt].x, f[nt].y);
-                            mma_bf16_16816(sacc[j][mt][nt], c, f[nt].z, f[nt].w);
+                            mma_f16_16816(sacc[j][mt][nt], a0[0], a1[0], a0[1], a1[1], f[nt].x, f[nt].y);
+                            mma_f16_16816(sacc[j][mt][nt], a0[2], a1[2], a0[3], a1[3], f[nt].z, f[nt].w);
                         }
                     }
             }
-            // ---- scores in log2 units; score(j, c, nt, x) is of key 32j + 4g + c, row 8nt + 2t + x
+            // ---- scores, in units of the row; score(j, c, nt, x) is of key 32j + 4g + c, row 8nt + 2t + x
             const auto score = [&](int j, int c, int nt, int x) -> float& { return sacc[j][c >> 1][nt][(c & 1) * 2 + x]; };
 #pragma unroll
             for (int j = 0; j < U; ++j)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const uint32_t head = K[(32 * j + 4 * g + c) * RW + D / 8];
-                    const float step = __uint_as_float(head << 16) * sl2, least = __uint_as_float(head & 0xffff0000u) * sl2;
+                    const float step = __uint_as_float(head << 16), least = __uint_as_float(head & 0xffff0000u);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -428,7 +493,8 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                         for (int c = 0; c < 4; c += 2) mx = max3f(mx, score(j, c, nt, x), score(j, c + 1, nt, x));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    m_new[nt][x] = max3f(mx, __shfl_xor_sync(0xffffffffu, mx, 16), m[nt][x]);
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    m_new[nt][x] = fmaxf(mx * unit[nt][x], m[nt][x]);
                     raise |= m_new[nt][x] > m[nt][x];
                 }
             if (__any_sync(0xffffffffu, raise)) {
@@ -467,7 +533,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             const float sc = score(j, c, nt, x);
-                            const float e = ex2_approx(sc + neg_m[nt][x]);
+                            const float e = ex2_approx(fmaf(sc, unit[nt][x], neg_m[nt][x]));
                             l[nt][x] += e;
                             if (masked && sc == -INFINITY) {  // such a key's step may be NaN
                                 w[x] = 0.f;
