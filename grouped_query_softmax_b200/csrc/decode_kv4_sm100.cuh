@@ -29,6 +29,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "sm100_ptx.cuh"
 
 namespace gqa {
@@ -109,7 +111,7 @@ __device__ __forceinline__ unsigned long long dec4_cut(unsigned long long total,
 // immediate only, and it would spend two on them; and the left shifts are products, which leave
 // the pipe of the shifts and logic operations, the kernel's busiest, to the others.
 struct Dec4Bits {
-    uint32_t mask, base, mask_even, base_even, mask_odd, base_odd, four, eight;
+    uint32_t mask, base, mask_even, base_even, mask_odd, base_odd, four, eight, half;
     __device__ __forceinline__ Dec4Bits() {
         asm volatile("mov.b32 %0, 0x00780078;" : "=r"(mask));
         asm volatile("mov.b32 %0, 0x41804180;" : "=r"(base));
@@ -119,12 +121,16 @@ struct Dec4Bits {
         asm volatile("mov.b32 %0, 0x4C004C00;" : "=r"(base_odd));
         asm volatile("mov.b32 %0, 4;" : "=r"(four));
         asm volatile("mov.b32 %0, 8;" : "=r"(eight));
+        asm volatile("mov.b32 %0, 0x10000;" : "=r"(half));
     }
     static __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t o) {
         uint32_t d;
         asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "r"(m), "r"(o));  // (x & m) | o
         return d;
     }
+    // the step and the minimum of a row from its last word
+    __device__ __forceinline__ float step(uint32_t head) const { return __uint_as_float(head * half); }
+    __device__ __forceinline__ float least(uint32_t head) const { return __uint_as_float(head & 0xffff0000u); }
     // bf16 16 + c
     template <int e>
     __device__ __forceinline__ uint32_t codes(uint32_t w) const {
@@ -457,7 +463,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const uint32_t head = K[(32 * j + 4 * g + c) * RW + D / 8];
-                    const float step = __uint_as_float(head << 16), least = __uint_as_float(head & 0xffff0000u);
+                    const float step = bits.step(head), least = bits.least(head);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -520,31 +526,37 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
 #pragma unroll
                 for (int x = 0; x < 2; ++x) neg_m[nt][x] = m[nt][x] == -INFINITY ? 0.f : -m[nt][x];
             uint32_t pb[U][NT][4];  // B operand: keys 8t + c and 8t + 4 + c of query row g
+            const auto weigh = [&](auto masked_keys) {
+                constexpr bool kMasked = decltype(masked_keys)::value;
 #pragma unroll
-            for (int j = 0; j < U; ++j)
+                for (int j = 0; j < U; ++j)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t head = V[(32 * j + 4 * g + c) * RW + D / 8];
-                    const float step = __uint_as_float(head << 16);
-                    const float mid = fmaf(8.f, step, __uint_as_float(head & 0xffff0000u));
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t head = V[(32 * j + 4 * g + c) * RW + D / 8];
+                        const float step = bits.step(head), mid = fmaf(8.f, step, bits.least(head));
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float w[2];
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float w[2];
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float sc = score(j, c, nt, x);
-                            const float e = ex2_approx(fmaf(sc, unit[nt][x], neg_m[nt][x]));
-                            l[nt][x] += e;
-                            if (masked && sc == -INFINITY) {  // such a key's step may be NaN
-                                w[x] = 0.f;
-                            } else {
-                                w[x] = e * step;
-                                beta[nt][x] = fmaf(e, mid, beta[nt][x]);
+                            for (int x = 0; x < 2; ++x) {
+                                const float sc = score(j, c, nt, x);
+                                const float e = ex2_approx(fmaf(sc, unit[nt][x], neg_m[nt][x]));
+                                l[nt][x] += e;
+                                if (kMasked && sc == -INFINITY) {  // such a key's step may be NaN
+                                    w[x] = 0.f;
+                                } else {
+                                    w[x] = e * step;
+                                    beta[nt][x] = fmaf(e, mid, beta[nt][x]);
+                                }
                             }
+                            pb[j][nt][c] = movmatrix_trans(pack_bf16x2(w[0], w[1]));
                         }
-                        pb[j][nt][c] = movmatrix_trans(pack_bf16x2(w[0], w[1]));
                     }
-                }
+            };
+            if (masked)
+                weigh(std::true_type{});
+            else
+                weigh(std::false_type{});
             // ---- O^T += V^T P^T
             const uint32_t* vr = V + 8 * t * RW + g;
 #pragma unroll
