@@ -104,53 +104,33 @@ __device__ __forceinline__ unsigned long long dec4_cut(unsigned long long total,
     return total * i / ctas;  // total is below 2^52 (checked on the host), i a few hundred
 }
 
-// Pairs of codes, nibble e of a word's low half and of its high half, as numbers offset + c: one
-// shift and one logic operation in bf16 (16 + c is the bits 0x4180 | c << 3), one and a half in
-// fp16, whose ten mantissa bits hold two nibbles (256 + c at bits 2-5, 16 + c at bits 6-9). The
-// constants come in registers that the compiler cannot see through: a logic operation takes one
-// immediate only, and it would spend two on them; and the left shifts are products, which leave
-// the pipe of the shifts and logic operations, the kernel's busiest, to the others.
-struct Dec4Bits {
-    uint32_t mask, base, mask_even, base_even, mask_odd, base_odd, four, eight, half;
-    __device__ __forceinline__ Dec4Bits() {
-        asm volatile("mov.b32 %0, 0x00780078;" : "=r"(mask));
-        asm volatile("mov.b32 %0, 0x41804180;" : "=r"(base));
-        asm volatile("mov.b32 %0, 0x003C003C;" : "=r"(mask_even));
-        asm volatile("mov.b32 %0, 0x5C005C00;" : "=r"(base_even));
-        asm volatile("mov.b32 %0, 0x03C003C0;" : "=r"(mask_odd));
-        asm volatile("mov.b32 %0, 0x4C004C00;" : "=r"(base_odd));
-        asm volatile("mov.b32 %0, 4;" : "=r"(four));
-        asm volatile("mov.b32 %0, 8;" : "=r"(eight));
-        asm volatile("mov.b32 %0, 0x10000;" : "=r"(half));
-    }
-    static __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t o) {
-        uint32_t d;
-        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "r"(m), "r"(o));  // (x & m) | o
-        return d;
-    }
-    // the step and the minimum of a row from its last word
-    __device__ __forceinline__ float step(uint32_t head) const { return __uint_as_float(head * half); }
-    __device__ __forceinline__ float least(uint32_t head) const { return __uint_as_float(head & 0xffff0000u); }
-    // bf16 16 + c
-    template <int e>
-    __device__ __forceinline__ uint32_t codes(uint32_t w) const {
-        return and_or(e == 0 ? w * eight : w >> (4 * e - 3), mask, base);
-    }
-    // fp16: 256 + c of nibbles 0 and 2, 16 + c of nibbles 1 and 3
-    __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&d)[4]) const {
-        const uint32_t lo = w * four, hi = w >> 6;
-        d[0] = and_or(lo, mask_even, base_even);
-        d[1] = and_or(lo, mask_odd, base_odd);
-        d[2] = and_or(hi, mask_even, base_even);
-        d[3] = and_or(hi, mask_odd, base_odd);
-    }
-};
+// Codes as fp16 numbers without a conversion: below 2^-14 the format is linear, so the bits of a
+// code are the number c * 2^-24, and four bits up 16 c * 2^-24. Pairs of nibbles e of a word's low
+// half and of its high half: e = 0, 2 at factor 1, e = 1, 3 at factor 16.
+__device__ __forceinline__ void dec4_codes(uint32_t w, uint32_t (&d)[4]) {
+    const uint32_t up = w >> 8;
+    d[0] = w & 0x000F000Fu;
+    d[1] = w & 0x00F000F0u;
+    d[2] = up & 0x000F000Fu;
+    d[3] = up & 0x00F000F0u;
+}
+// The step and the minimum of a row from its last word.
+__device__ __forceinline__ float dec4_step(uint32_t head) { return __uint_as_float(head << 16); }
+__device__ __forceinline__ float dec4_least(uint32_t head) { return __uint_as_float(head & 0xffff0000u); }
+__device__ __forceinline__ uint32_t dec4_halves(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Exponent field e of |x| for scaling x to [2^14, 2^15) by 2^(141 - e), whose own field is 268 - e,
+// and products with the codes back by 2^24 times the inverse, field e + 10; kept where both are
+// normal numbers (|x| from 2^-112 to 2^118).
+__device__ __forceinline__ int dec4_exponent(float x) { return min(max((int)(__float_as_uint(x) >> 23), 15), 244); }
+__device__ __forceinline__ float dec4_pow2(int field) { return __uint_as_float((uint32_t)field << 23); }
+
 // D = A(16x16 fp16, row) * B(16x8 fp16, col) + C, fp32 accumulate.
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                               uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -248,7 +228,6 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
     unsigned long long seq0 = ctl->first;
     Dec4Seq s = dec4_seq(p, b);
 
-    const Dec4Bits bits;
     const int box = min(p.page_size, kD4Keys);  // rows of one bulk copy
     const int boxes = kD4Keys / box;
     const int page_step = kWarps * kD4Keys / p.page_size, row_step = kWarps * kD4Keys - page_step * p.page_size;
@@ -320,17 +299,18 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
             st = st + 1 == kStages ? 0 : st + 1;
         }
 
-        // ---- Q fragments: lane (g, t) holds words t + 4i of row g's elements, as pairs (e, e + 4).
-        // They are fp16, each row times the power of two that takes its largest element to [2^7, 2^8):
-        // exact (fp16 has three bits more) down to 2^-24 of the largest, and off by at most 2^-33 of
-        // it below. A row with an infinity or a NaN keeps it, and zeros stay zeros.
+        // ---- Q fragments: lane (g, t) holds words t + 4i of row g's elements, as pairs (e, e + 4), the
+        // odd ones divided by their codes' 16. Each row is taken times the power of two that brings
+        // its largest element to [2^14, 2^15): its fp16 form is then exact (fp16 has three bits more)
+        // down to 2^-27 of the largest, and off by at most 2^-35 of it below. A row with an infinity
+        // or a NaN keeps it.
         uint4 qf[NT == 1 ? kKI : 1];
-        // of the rows 2t, 2t + 1 of each tile, in the scaled units: the sum, the sum times the codes'
-        // offsets, and the factor back to log2 units
-        float sumq[NT][2], offq[NT][2], unit[NT][2];
+        // of the rows 2t, 2t + 1 of each tile: the sum, in the products' units, and the factor from
+        // these to log2 units
+        float sumq[NT][2], unit[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float f[kKI][8], top = 0.f;
+            float f[kKI][8], top = 0.f, sum = 0.f;
             const bool row_ok = 8 * nt + g < nrows;
 #pragma unroll
             for (int i = 0; i < kKI; ++i) {
@@ -347,57 +327,48 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // exponents of the factor and its inverse, both of normal numbers
-            const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 254);
-            const float up = __uint_as_float((uint32_t)(261 - ex) << 23), down = __uint_as_float((uint32_t)(ex - 7) << 23);
-            float sum = 0.f, even = 0.f;
+            const int ex = dec4_exponent(top);
+            const float up = dec4_pow2(268 - ex);
 #pragma unroll
             for (int i = 0; i < kKI; ++i) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     f[i][e] *= up;
                     sum += f[i][e];
-                    if (e % 2 == 0) even += f[i][e];
                 }
-                const auto pair = [&](int e) {
-                    const __half2 h = __floats2half2_rn(f[i][e], f[i][e + 4]);
-                    return *reinterpret_cast<const uint32_t*>(&h);
-                };
-                const uint4 v = make_uint4(pair(0), pair(1), pair(2), pair(3));
+                const uint4 v = make_uint4(dec4_halves(f[i][0], f[i][4]), dec4_halves(f[i][1] * 0.0625f, f[i][5] * 0.0625f),
+                                           dec4_halves(f[i][2], f[i][6]), dec4_halves(f[i][3] * 0.0625f, f[i][7] * 0.0625f));
                 if constexpr (NT == 1)
                     qf[i] = v;
                 else if (warp == 0)
                     reinterpret_cast<uint4*>(dec4_smem + C::kQOff)[(i * NT + nt) * 32 + lane] = v;
             }
-            float off = fmaf(240.f, even, 16.f * sum);
-#pragma unroll
-            for (int d = 1; d < 4; d <<= 1) {
-                sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                off += __shfl_xor_sync(0xffffffffu, off, d);
-            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                sumq[nt][x] = __shfl_sync(0xffffffffu, sum, 8 * t + 4 * x);
-                offq[nt][x] = -__shfl_sync(0xffffffffu, off, 8 * t + 4 * x);
-                unit[nt][x] = __shfl_sync(0xffffffffu, down, 8 * t + 4 * x) * p.scale_log2;
+                sumq[nt][x] = __shfl_sync(0xffffffffu, sum, 8 * t + 4 * x) * 0x1p-24f;
+                unit[nt][x] = __shfl_sync(0xffffffffu, dec4_pow2(ex + 10), 8 * t + 4 * x) * p.scale_log2;
             }
         }
         if constexpr (NT > 1) __syncthreads();
 
         float m[NT][2], l[NT][2], beta[NT][2];
-        float oacc[kMT][NT][4], ones[NT][4];
+        float oacc[kMT][NT][4], eights[NT][4];
+        float top_step = 0.f, up_step = dec4_pow2(268 - dec4_exponent(0.f));  // largest step yet, and w's factor
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = beta[nt][0] = beta[nt][1] = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                ones[nt][e] = 0.f;
+                eights[nt][e] = 0.f;
 #pragma unroll
                 for (int i = 0; i < kMT; ++i) oacc[i][nt][e] = 0.f;
             }
         }
         const int pos_min = s.len - p.Tq;                                          // position of row 0
+        const int lo_min = p.window > 0 ? s.len - min(p.window + p.Tq - 1, s.len) : 0;  // first key of the first row
         const int lo_max = p.window > 0 ? s.len - min(p.window, s.len) : -1;  // first key of the last row
 
         for (int it = 0; it < n_mine; ++it) {
@@ -426,10 +397,9 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        sacc[j][mt][nt][0] = sacc[j][mt][nt][2] = offq[nt][0];
-                        sacc[j][mt][nt][1] = sacc[j][mt][nt][3] = offq[nt][1];
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sacc[j][mt][nt][e] = 0.f;
             const uint32_t* kr = K + 4 * g * RW + t;
 #pragma unroll
             for (int i = 0; i < kKI; ++i) {
@@ -447,8 +417,8 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                     for (int mt = 0; mt < 2; ++mt) {
                         const uint32_t* w = kr + (32 * j + 2 * mt) * RW + 4 * i;
                         uint32_t a0[4], a1[4];
-                        bits.codes_f16(w[0], a0);
-                        bits.codes_f16(w[RW], a1);
+                        dec4_codes(w[0], a0);
+                        dec4_codes(w[RW], a1);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             mma_f16_16816(sacc[j][mt][nt], a0[0], a1[0], a0[1], a1[1], f[nt].x, f[nt].y);
@@ -463,7 +433,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const uint32_t head = K[(32 * j + 4 * g + c) * RW + D / 8];
-                    const float step = bits.step(head), least = bits.least(head);
+                    const float step = dec4_step(head), least = dec4_least(head);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -486,7 +456,22 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                                 if (32 * j + c > hi || 32 * j + c < lo) score(j, c, nt, x) = -INFINITY;
                     }
             }
-            bool raise = false;
+            // steps and middles of this lane's value rows; of a row that no query sees they may be anything
+            float vstep[U][4], vmid[U][4], top = 0.f;
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t head = V[(32 * j + 4 * g + c) * RW + D / 8];
+                    if (masked) {
+                        const int key = key0 + 32 * j + 4 * g + c;
+                        if (key >= s.len || key < lo_min) head = 0u;
+                    }
+                    vstep[j][c] = dec4_step(head);
+                    vmid[j][c] = fmaf(8.f, vstep[j][c], dec4_least(head));
+                    top = fmaxf(top, fabsf(vstep[j][c]));
+                }
+            bool raise = top > top_step;
             float m_new[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -504,6 +489,13 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                     raise |= m_new[nt][x] > m[nt][x];
                 }
             if (__any_sync(0xffffffffu, raise)) {
+                // w = p * step is scaled so that the largest step yet is in [2^14, 2^15)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                top_step = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)), top_step);
+                const int ex = dec4_exponent(top_step);
+                const float down = dec4_pow2(268 - ex) / up_step;  // a power of two, or 0 past fp32's range
+                up_step = dec4_pow2(268 - ex);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -512,11 +504,12 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                         m[nt][x] = m_new[nt][x];
                         l[nt][x] *= alpha;
                         beta[nt][x] *= alpha;
-                        ones[nt][x] *= alpha;  // its four rows are alike: only the first two are used
+                        const float both = alpha * down;
+                        eights[nt][x] *= both;  // its rows are alike: only the first is used
 #pragma unroll
                         for (int i = 0; i < kMT; ++i) {
-                            oacc[i][nt][x] *= alpha;
-                            oacc[i][nt][x + 2] *= alpha;
+                            oacc[i][nt][x] *= both;
+                            oacc[i][nt][x + 2] *= both;
                         }
                     }
             }
@@ -531,11 +524,9 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
 #pragma unroll
                 for (int j = 0; j < U; ++j)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t head = V[(32 * j + 4 * g + c) * RW + D / 8];
-                        const float step = bits.step(head), mid = fmaf(8.f, step, bits.least(head));
+                    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
+                        for (int c = 0; c < 4; ++c) {
                             float w[2];
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
@@ -545,11 +536,11 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                                 if (kMasked && sc == -INFINITY) {  // such a key's step may be NaN
                                     w[x] = 0.f;
                                 } else {
-                                    w[x] = e * step;
-                                    beta[nt][x] = fmaf(e, mid, beta[nt][x]);
+                                    w[x] = e * (vstep[j][c] * up_step);
+                                    beta[nt][x] = fmaf(e, vmid[j][c], beta[nt][x]);
                                 }
                             }
-                            pb[j][nt][c] = movmatrix_trans(pack_bf16x2(w[0], w[1]));
+                            pb[j][nt][c] = movmatrix_trans(dec4_halves(w[0], w[1]));
                         }
                     }
             };
@@ -562,42 +553,29 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
 #pragma unroll
             for (int ks = 0; ks < 2 * U; ++ks) {  // 16 keys: sets c0, c0 + 1 of group ks / 2
                 const int c0 = ks % 2 * 2;
-                uint32_t lo[2][kVI], hi[2][kVI];
+                uint32_t lo[2][kVI][4], hi[2][kVI][4];  // elements 0-3 and 4-7 of the words
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int i = 0; i < kVI; ++i) {
                         const uint32_t* w = vr + (32 * (ks / 2) + c0 + c) * RW + 8 * i;
-                        lo[c][i] = __byte_perm(w[0], w[4 * RW], 0x5410);
-                        hi[c][i] = __byte_perm(w[0], w[4 * RW], 0x7632);
+                        dec4_codes(__byte_perm(w[0], w[4 * RW], 0x5410), lo[c][i]);
+                        dec4_codes(__byte_perm(w[0], w[4 * RW], 0x7632), hi[c][i]);
                     }
                 const auto product = [&](float (&acc)[NT][4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-                    const uint32_t a[4] = {a0, a1, a2, a3};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(acc[nt], a, pb[ks / 2][nt][c0], pb[ks / 2][nt][c0 + 1]);
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16_16816(acc[nt], a0, a1, a2, a3, pb[ks / 2][nt][c0], pb[ks / 2][nt][c0 + 1]);
                 };
-                constexpr uint32_t kOne = 0x3F803F80u;
-                product(ones, kOne, kOne, kOne, kOne);
-                if constexpr (D == 128) {  // rows g, g + 8 of tile e: d = 8g + e, 64 + 8g + e
-#define GQA_D4_HALF(x, e, tile) \
-    product(oacc[tile], bits.template codes<e>(x[0][0]), bits.template codes<e>(x[0][1]), bits.template codes<e>(x[1][0]), bits.template codes<e>(x[1][1]))
-                    GQA_D4_HALF(lo, 0, 0);
-                    GQA_D4_HALF(lo, 1, 1);
-                    GQA_D4_HALF(lo, 2, 2);
-                    GQA_D4_HALF(lo, 3, 3);
-                    GQA_D4_HALF(hi, 0, 4);
-                    GQA_D4_HALF(hi, 1, 5);
-                    GQA_D4_HALF(hi, 2, 6);
-                    GQA_D4_HALF(hi, 3, 7);
-#undef GQA_D4_HALF
-                } else {  // rows g, g + 8 of tile e: d = 8g + e, 8g + 4 + e
-#define GQA_D4_ALL(e) \
-    product(oacc[e], bits.template codes<e>(lo[0][0]), bits.template codes<e>(hi[0][0]), bits.template codes<e>(lo[1][0]), bits.template codes<e>(hi[1][0]))
-                    GQA_D4_ALL(0);
-                    GQA_D4_ALL(1);
-                    GQA_D4_ALL(2);
-                    GQA_D4_ALL(3);
-#undef GQA_D4_ALL
+                product(eights, 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (D == 128) {  // rows g, g + 8 of tile e: d = 8g + e, 64 + 8g + e
+                        product(oacc[e], lo[0][0][e], lo[0][kVI - 1][e], lo[1][0][e], lo[1][kVI - 1][e]);
+                        product(oacc[kMT / 2 + e], hi[0][0][e], hi[0][kVI - 1][e], hi[1][0][e], hi[1][kVI - 1][e]);
+                    } else {  // rows g, g + 8 of tile e: d = 8g + e, 8g + 4 + e
+                        product(oacc[e], lo[0][0][e], hi[0][0][e], lo[1][0][e], hi[1][0][e]);
+                    }
                 }
             }
             __syncwarp();  // every lane has read the stage
@@ -624,12 +602,13 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                     area[n] = m[nt][x];
                     area[C::kRows + n] = l[nt][x];
                 }
-                const float shift = fmaf(-24.f, ones[nt][x], beta[nt][x]);
+                const float down = dec4_pow2(dec4_exponent(top_step) + 10);  // 2^24 / up_step
                 float* out = area + 2 * C::kRows + n * D + 8 * g;
 #pragma unroll
                 for (int i = 0; i < kMT; ++i) {
-                    out[i] = oacc[i][nt][x] + shift;
-                    out[(D == 128 ? 64 : 4) + i] = oacc[i][nt][x + 2] + shift;
+                    const float f = i % 2 ? 0.0625f : 1.f;  // odd elements' codes count 16 times
+                    out[i] = fmaf(fmaf(oacc[i][nt][x], f, -eights[nt][x]), down, beta[nt][x]);
+                    out[(D == 128 ? 64 : 4) + i] = fmaf(fmaf(oacc[i][nt][x + 2], f, -eights[nt][x]), down, beta[nt][x]);
                 }
             }
         __syncthreads();
