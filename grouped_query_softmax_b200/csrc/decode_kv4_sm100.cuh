@@ -549,19 +549,10 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
             else
                 weigh(std::false_type{});
             // ---- O^T += V^T P^T
-            const uint32_t* vr = V + 8 * t * RW + g;
+            const uint32_t* vr = V + 4 * g * RW + t;
 #pragma unroll
             for (int ks = 0; ks < 2 * U; ++ks) {  // 16 keys: sets c0, c0 + 1 of group ks / 2
                 const int c0 = ks % 2 * 2;
-                uint32_t lo[2][kVI][4], hi[2][kVI][4];  // elements 0-3 and 4-7 of the words
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int i = 0; i < kVI; ++i) {
-                        const uint32_t* w = vr + (32 * (ks / 2) + c0 + c) * RW + 8 * i;
-                        dec4_codes(__byte_perm(w[0], w[4 * RW], 0x5410), lo[c][i]);
-                        dec4_codes(__byte_perm(w[0], w[4 * RW], 0x7632), hi[c][i]);
-                    }
                 const auto product = [&](float (&acc)[NT][4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -569,13 +560,17 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                 };
                 product(eights, 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (D == 128) {  // rows g, g + 8 of tile e: d = 8g + e, 64 + 8g + e
-                        product(oacc[e], lo[0][0][e], lo[0][kVI - 1][e], lo[1][0][e], lo[1][kVI - 1][e]);
-                        product(oacc[kMT / 2 + e], hi[0][0][e], hi[0][kVI - 1][e], hi[1][0][e], hi[1][kVI - 1][e]);
-                    } else {  // rows g, g + 8 of tile e: d = 8g + e, 8g + 4 + e
-                        product(oacc[e], lo[0][0][e], hi[0][0][e], lo[1][0][e], hi[1][0][e]);
-                    }
+                for (int i = 0; i < kVI; ++i) {
+                    // transposed, a word's halves (four codes each) of keys 4g + c become those of keys
+                    // 8t + c and 8t + 4 + c; rows g, g + 8 of tile 4i + e: d = 64i + 4g + e, 64i + 32 + 4g + e
+                    uint32_t v[2][2][4];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            dec4_codes(movmatrix_trans(vr[(32 * (ks / 2) + c0 + c) * RW + 8 * i + 4 * r]), v[c][r]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) product(oacc[4 * i + e], v[0][0][e], v[0][1][e], v[1][0][e], v[1][1][e]);
                 }
             }
             __syncwarp();  // every lane has read the stage
@@ -603,12 +598,12 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                     area[C::kRows + n] = l[nt][x];
                 }
                 const float down = dec4_pow2(dec4_exponent(top_step) + 10);  // 2^24 / up_step
-                float* out = area + 2 * C::kRows + n * D + 8 * g;
+                float* out = area + 2 * C::kRows + n * D + 4 * g;
 #pragma unroll
                 for (int i = 0; i < kMT; ++i) {
                     const float f = i % 2 ? 0.0625f : 1.f;  // odd elements' codes count 16 times
-                    out[i] = fmaf(fmaf(oacc[i][nt][x], f, -eights[nt][x]), down, beta[nt][x]);
-                    out[(D == 128 ? 64 : 4) + i] = fmaf(fmaf(oacc[i][nt][x + 2], f, -eights[nt][x]), down, beta[nt][x]);
+                    out[64 * (i / 4) + i % 4] = fmaf(fmaf(oacc[i][nt][x], f, -eights[nt][x]), down, beta[nt][x]);
+                    out[64 * (i / 4) + 32 + i % 4] = fmaf(fmaf(oacc[i][nt][x + 2], f, -eights[nt][x]), down, beta[nt][x]);
                 }
             }
         __syncthreads();
