@@ -19,12 +19,11 @@
 // different banks without padding or swizzle. P goes from its accumulator layout to the B
 // operand's with one 8x8 transpose a tile.
 //
-// Work: the tiles of 64 keys of every (sequence, KV head, row chunk) laid end to end are cut
-// into equal runs, one per CTA, so all CTAs finish together whatever the lengths. In a CTA the
-// warps take tiles in turn, each with a ring of its own that its own lanes fill with bulk
-// copies (a page's rows of one head are contiguous): no warp waits for another until the
-// piece ends. A unit cut between CTAs leaves fp32 partials that a second kernel merges in
-// a fixed order. Bound by HBM: D + 8 bytes a key and KV head.
+// Work: the tiles of every (sequence, KV head, row chunk) laid end to end are cut into equal runs,
+// one per warp, so all warps finish together whatever the lengths. A warp has a ring of its own
+// that its own lanes fill with bulk copies (a page's rows of one head are contiguous): no warp
+// waits for another. A unit cut between warps leaves fp32 partials that a second kernel merges
+// in a fixed order. Bound by HBM: D + 8 bytes a key and KV head.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -35,9 +34,7 @@
 
 namespace gqa {
 
-constexpr int kD4Keys = 64;  // keys a tile: two groups of 32, the keys of two m16 tiles
-constexpr int kD4Groups = kD4Keys / 32;
-constexpr int kD4MergeThreads = 256;
+constexpr int kD4MergeWarps = 4;
 
 struct Dec4Params {
     const __nv_bfloat16* q;  // [B, Hq, Tq, D]
@@ -51,36 +48,38 @@ struct Dec4Params {
     int n_rc;  // chunks of query rows a group
     int page_size, num_pages, max_pages, capacity, window;
     float scale_log2;
-    float* part;      // [2 * gridDim.x, rows, D] partial outputs
-    float* part_lse;  // [2 * gridDim.x, rows] log2-domain log-sum-exp
+    float* part;      // [2 * warps, rows, D] partial outputs
+    float* part_lse;  // [2 * warps, rows] log2-domain log-sum-exp
+    unsigned long long* start;  // [B + 1] tiles before each sequence, and all of them
     uint32_t* err;
     unsigned long long timeout_ns;
 };
 
 template <int D, int NT>
 struct Dec4Cfg {
-    static constexpr int kRows = 8 * NT;            // query rows a CTA takes
-    static constexpr int kRow = D / 2 + 4;          // bytes of a stored row
-    static constexpr int kTile = kD4Keys * kRow;    // K or V rows of a tile
+    static constexpr int kRows = 8 * NT;                // query rows a warp takes
+    static constexpr int kRow = D / 2 + 4;              // bytes of a stored row
+    static constexpr int kGroups = NT == 1 ? 2 : 1;     // groups of 32 keys (two m16 tiles) in a tile
+    static constexpr int kKeys = 32 * kGroups;
+    static constexpr int kTile = kKeys * kRow;          // K or V rows of a tile
     static constexpr int kStage = 2 * kTile;
-    static constexpr int kStages = 2;
+    static constexpr int kStages = NT == 1 ? 2 : NT == 2 ? 3 : 4;
     static constexpr int kWarps = NT == 4 ? 8 : 6;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kCtasPerSm = NT == 4 ? 1 : 2;
-    static constexpr int kWarpBytes = kStages * kStage;
-    static constexpr int kQOff = kWarps * kWarpBytes;
-    static constexpr int kQBytes = NT == 1 ? 0 : (D / 32) * NT * 32 * 16;  // Q fragments
-    static constexpr int kCtlOff = kQOff + kQBytes;
+    static constexpr int kQBytes = NT == 1 ? 0 : (D / 32) * NT * 32 * 16;  // Q fragments, in registers for one tile
+    static constexpr int kWarpBytes = kStages * kStage + kQBytes;
+    static constexpr int kCtlOff = kWarps * kWarpBytes;
     struct Ctl {
         uint64_t full[kWarps][kStages];
         unsigned long long sums[kWarps];
-        unsigned long long first;  // work before the sequence that holds this CTA's first tile
-        int b;                     // that sequence
+        unsigned long long first[kWarps];  // tiles before the sequence that holds a warp's first one
+        int b[kWarps];                     // that sequence
         uint32_t abort;
     };
     static constexpr int kBytes = kCtlOff + (int)sizeof(Ctl);
-    static_assert((kRows * D + 2 * kRows) * 4 <= kWarpBytes, "a warp merges through its ring");
-    static_assert(kTile % 16 == 0 && kStage % 16 == 0 && kCtlOff % 16 == 0, "bulk copies need 16 bytes");
+    static_assert(kTile % 16 == 0 && kWarpBytes % 16 == 0, "bulk copies need 16 bytes");
+    static_assert(kCtasPerSm * (kBytes + 1024) <= 233472, "shared memory of an SM");
 };
 
 // Tiles of one sequence: [first, first + n). A valid sequence has at least one, so that the
@@ -88,20 +87,22 @@ struct Dec4Cfg {
 struct Dec4Seq {
     int len, first, n;
 };
+template <int kKeys>
 __device__ __forceinline__ Dec4Seq dec4_seq(const Dec4Params& p, int b) {
     Dec4Seq s;
     s.len = __ldg(p.seqlens + b);
     s.first = s.n = 0;
     if (s.len < 0 || s.len > p.capacity) return s;
     const long long lo = p.window > 0 ? (long long)s.len - p.Tq - p.window + 1 : 0;
-    s.first = lo > 0 ? (int)(lo / kD4Keys) : 0;
-    s.n = max(1, (s.len + kD4Keys - 1) / kD4Keys - s.first);
+    s.first = lo > 0 ? (int)(lo / kKeys) : 0;
+    s.n = max(1, (s.len + kKeys - 1) / kKeys - s.first);
     return s;
 }
 
-// Start of CTA i's run when `total` tiles are cut into `ctas` runs.
-__device__ __forceinline__ unsigned long long dec4_cut(unsigned long long total, unsigned i, unsigned ctas) {
-    return total * i / ctas;  // total is below 2^52 (checked on the host), i a few hundred
+// Start of run i when `total` tiles are cut into `runs`; total is below 2^52 (checked on the host)
+// and runs at most a few thousand.
+__device__ __forceinline__ unsigned long long dec4_cut(unsigned long long total, unsigned i, unsigned runs) {
+    return total * i / runs;
 }
 
 // Codes as fp16 numbers without a conversion: below 2^-14 the format is linear, so the bits of a
@@ -140,37 +141,13 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
     return d;
 }
 
-// All threads of the block: the sum over sequences of f(b), and the sum over b < upto.
-template <int kWarps, class F>
-__device__ __forceinline__ void dec4_sums(int B, int upto, unsigned long long* warp_sums, F f, unsigned long long* before,
-                                          unsigned long long* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    unsigned long long v[2] = {0, 0};
-    for (int b = threadIdx.x; b < B; b += 32 * kWarps) {
-        const unsigned long long x = f(b);
-        v[0] += x;
-        if (b < upto) v[1] += x;
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
-        if (lane == 0) warp_sums[warp] = v[i];
-        __syncthreads();
-        v[i] = 0;
-        for (int w = 0; w < kWarps; ++w) v[i] += warp_sums[w];
-        __syncthreads();
-    }
-    *total = v[0];
-    *before = v[1];
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_decode_kv4_kernel(const Dec4Params p) {
     using C = Dec4Cfg<D, NT>;
     constexpr int kStages = C::kStages;
     constexpr int kWarps = C::kWarps;
-    constexpr int U = kD4Groups;
+    constexpr int U = C::kGroups;
+    constexpr int kKeys = C::kKeys;
     constexpr int RW = C::kRow / 4;  // words of a stored row
     constexpr int kKI = D / 32;      // word groups of a key row: four words, one a lane of a quad
     constexpr int kVI = D / 64;      // word groups of a value row: eight words, one a quad
@@ -188,49 +165,67 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
         fence_mbar_init();
     }
 
-    // ---- this CTA's run of tiles and the sequence it starts in
+    // ---- this warp's run of tiles and the sequence it starts in. Neighbouring runs go to
+    // different CTAs, so that few tiles spread over all SMs.
     const int units = p.Hkv * p.n_rc;  // units of a sequence
-    const auto work_of = [&](int b) { return (unsigned long long)dec4_seq(p, b).n * units; };
-    unsigned long long total, before;
-    dec4_sums<kWarps>(p.B, 0, ctl->sums, work_of, &before, &total);
-    const unsigned ctas = (unsigned)min((unsigned long long)gridDim.x, total);
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < p.B; b += C::kThreads)
-            if (dec4_seq(p, b).n == 0) atomicOr(p.err, kDevErrBadSeqlens);
-    if (blockIdx.x >= ctas) return;
-    unsigned long long at = dec4_cut(total, blockIdx.x, ctas);
-    const unsigned long long end = dec4_cut(total, blockIdx.x + 1, ctas);
-    {
-        unsigned long long run = 0;  // work before this round's sequences
-        for (int b0 = 0; b0 < p.B && run <= at; b0 += C::kThreads) {
-            const int b = b0 + threadIdx.x;
-            const unsigned long long x = b < p.B ? work_of(b) : 0;
-            unsigned long long inc = x;
+    const auto work_of = [&](int b) { return b < p.B ? (unsigned long long)dec4_seq<kKeys>(p, b).n * units : 0ull; };
+    const unsigned run = warp * gridDim.x + blockIdx.x;
+    const bool one_pass = p.B <= C::kThreads;
+    unsigned long long total = 0;
+    if (!one_pass) {
+        for (int b = threadIdx.x; b < p.B; b += C::kThreads) total += work_of(b);
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, d);
-                if (lane >= d) inc += y;
-            }
-            if (lane == 31) ctl->sums[warp] = inc;
-            __syncthreads();
-            unsigned long long base = run;
-            for (int w = 0; w < warp; ++w) base += ctl->sums[w];
-            const unsigned long long lo = base + inc - x;
-            if (x > 0 && lo <= at && at < lo + x) {
-                ctl->b = b;
-                ctl->first = lo;
-            }
-            for (int w = 0; w < kWarps; ++w) run += ctl->sums[w];
-            __syncthreads();
-        }
+        for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+        if (lane == 0) ctl->sums[warp] = total;
+        __syncthreads();
+        total = 0;
+        for (int w = 0; w < kWarps; ++w) total += ctl->sums[w];
+        __syncthreads();
     }
-    int b = ctl->b;
-    unsigned long long seq0 = ctl->first;
-    Dec4Seq s = dec4_seq(p, b);
+    unsigned runs = 0;
+    unsigned long long before = 0;  // tiles of the rounds of sequences already seen
+    for (int b0 = 0; b0 < p.B; b0 += C::kThreads) {
+        const int b = b0 + threadIdx.x;
+        const unsigned long long x = work_of(b);
+        unsigned long long inc = x;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += y;
+        }
+        if (lane == 31) ctl->sums[warp] = inc;
+        __syncthreads();
+        unsigned long long lo = before + inc - x;
+        for (int w = 0; w < warp; ++w) lo += ctl->sums[w];
+        for (int w = 0; w < kWarps; ++w) before += ctl->sums[w];
+        if (one_pass) total = before;
+        runs = (unsigned)min((unsigned long long)gridDim.x * kWarps, total);
+        for (int w = 0; w < kWarps; ++w) {
+            const unsigned r = w * gridDim.x + blockIdx.x;
+            const unsigned long long first = r < runs ? dec4_cut(total, r, runs) : total;
+            if (lo <= first && first < lo + x) {
+                ctl->b[w] = b;
+                ctl->first[w] = lo;
+            }
+        }
+        if (blockIdx.x == 0 && b < p.B) {
+            if (p.start != nullptr) p.start[b] = lo;
+            if (x == 0) atomicOr(p.err, kDevErrBadSeqlens);
+        }
+        __syncthreads();
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.start != nullptr) p.start[p.B] = total;
+    if (run >= runs) return;
+    unsigned long long at = dec4_cut(total, run, runs);
+    const unsigned long long end = dec4_cut(total, run + 1, runs);
+    int b = ctl->b[warp];
+    unsigned long long seq0 = ctl->first[warp];
+    Dec4Seq s = dec4_seq<kKeys>(p, b);
 
-    const int box = min(p.page_size, kD4Keys);  // rows of one bulk copy
-    const int boxes = kD4Keys / box;
-    const int page_step = kWarps * kD4Keys / p.page_size, row_step = kWarps * kD4Keys - page_step * p.page_size;
+    const int box = min(p.page_size, kKeys);  // rows of one bulk copy
+    const int boxes = kKeys / box;
+    const unsigned all_boxes = (1u << boxes) - 1;
+    const int page_step = kKeys / p.page_size, row_step = kKeys - page_step * p.page_size;
     volatile uint32_t* abort_flag = &ctl->abort;
     int stage = 0;
     uint32_t phase = 0;
@@ -238,7 +233,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
     while (at < end) {
         while (at >= seq0 + (unsigned long long)s.n * units) {  // sequences without work have n = 0
             seq0 += (unsigned long long)s.n * units;
-            s = dec4_seq(p, ++b);
+            s = dec4_seq<kKeys>(p, ++b);
         }
         // ---- the piece: tiles [t0, t1) of unit u of sequence b
         const unsigned long long in_seq = at - seq0;
@@ -250,42 +245,44 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
         const int rbase = rc * C::kRows;
         const int nrows = min(C::kRows, p.G * p.Tq - rbase);
         const size_t row0 = ((size_t)b * p.Hq + (size_t)h * p.G) * p.Tq + rbase;
-        const int key_base = (s.first + t0) * kD4Keys;
-        const int n_mine = (t1 - t0 - warp + kWarps - 1) / kWarps;  // tiles warp, warp + kWarps, ...
+        const int key_base = (s.first + t0) * kKeys;
+        const int n_tiles = t1 - t0;
         const uint8_t* k_head = p.k + h * p.k_sh;
         const uint8_t* v_head = p.v + h * p.v_sh;
 
         // The next tile to fetch: this lane's box starts at key next_key, row next_row of pool page
-        // next_page (-1: none), which is looked up one tile ahead of its copy.
-        int next_key = key_base + warp * kD4Keys + lane * box;
+        // next_page (-1: outside the pool, -2: no box), which is looked up one tile ahead of its copy.
+        int next_key = key_base + lane * box;
         int ord = next_key / p.page_size, next_row = next_key - ord * p.page_size;
         const int* table = p.table + (size_t)b * p.max_pages;
-        const auto look_up = [&]() { return lane < boxes && next_key < s.len ? __ldg(table + ord) : -1; };
+        const auto look_up = [&]() {
+            if (lane >= boxes || next_key >= s.len) return -2;
+            const int pg = __ldg(table + ord);
+            return (unsigned)pg < (unsigned)p.num_pages ? pg : -1;
+        };
         int next_page = look_up();
         // Copy the next tile into ring stage st. Boxes past the sequence are left out (their keys
         // are masked); a page number outside the pool reads as rows of zeros.
         const auto fetch = [&](int st) {
-            const bool want = lane < boxes && next_key < s.len;
-            const bool ok = want && (unsigned)next_page < (unsigned)p.num_pages;
-            const unsigned oks = __ballot_sync(0xffffffffu, ok), wants = __ballot_sync(0xffffffffu, want);
-            const uint32_t bar = bars + 8 * st, dst = ring_addr + st * C::kStage + lane * box * C::kRow;
+            const unsigned oks = __ballot_sync(0xffffffffu, next_page >= 0);
+            const uint32_t bar = bars + 8 * st;
+            const int dst = st * C::kStage + lane * box * C::kRow;
             if (lane == 0) mbar_arrive_expect_tx(bar, __popc(oks) * 2 * box * C::kRow);
             __syncwarp();
-            if (ok) {
+            if (next_page >= 0) {
                 const long long row = (long long)next_row * C::kRow;
-                bulk_load(dst, k_head + next_page * p.k_sb + row, box * C::kRow, bar);
-                bulk_load(dst + C::kTile, v_head + next_page * p.v_sb + row, box * C::kRow, bar);
+                bulk_load(ring_addr + dst, k_head + next_page * p.k_sb + row, box * C::kRow, bar);
+                bulk_load(ring_addr + dst + C::kTile, v_head + next_page * p.v_sb + row, box * C::kRow, bar);
             }
-            if (oks != wants) {
-                for (int x = 0; x < boxes; ++x)
-                    if ((wants & ~oks) >> x & 1u)
-                        for (int e = lane; e < box * RW; e += 32) {
-                            uint32_t* z = reinterpret_cast<uint32_t*>(ring + st * C::kStage + x * box * C::kRow) + e;
-                            z[0] = z[C::kTile / 4] = 0u;
-                        }
-                fence_proxy_async_smem();  // before a later copy into these bytes
+            if (oks != all_boxes) {
+                if (next_page == -1) {
+                    uint32_t* z = reinterpret_cast<uint32_t*>(ring + dst);
+                    for (int e = 0; e < box * RW; ++e) z[e] = z[C::kTile / 4 + e] = 0u;
+                    fence_proxy_async_smem();  // before a later copy into these bytes
+                }
+                __syncwarp();
             }
-            next_key += kWarps * kD4Keys;
+            next_key += kKeys;
             ord += page_step;
             next_row += row_step;
             if (next_row >= p.page_size) {
@@ -294,7 +291,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
             }
             next_page = look_up();
         };
-        for (int i = 0, st = stage; i < kStages && i < n_mine; ++i) {
+        for (int i = 0, st = stage; i < kStages && i < n_tiles; ++i) {
             fetch(st);
             st = st + 1 == kStages ? 0 : st + 1;
         }
@@ -305,6 +302,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
         // down to 2^-27 of the largest, and off by at most 2^-35 of it below. A row with an infinity
         // or a NaN keeps it.
         uint4 qf[NT == 1 ? kKI : 1];
+        uint4* q_frags = reinterpret_cast<uint4*>(ring + kStages * C::kStage);
         // of the rows 2t, 2t + 1 of each tile: the sum, in the products' units, and the factor from
         // these to log2 units
         float sumq[NT][2], unit[NT][2];
@@ -340,8 +338,8 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                                            dec4_halves(f[i][2], f[i][6]), dec4_halves(f[i][3] * 0.0625f, f[i][7] * 0.0625f));
                 if constexpr (NT == 1)
                     qf[i] = v;
-                else if (warp == 0)
-                    reinterpret_cast<uint4*>(dec4_smem + C::kQOff)[(i * NT + nt) * 32 + lane] = v;
+                else
+                    q_frags[(i * NT + nt) * 32 + lane] = v;
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -351,7 +349,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                 unit[nt][x] = __shfl_sync(0xffffffffu, dec4_pow2(ex + 10), 8 * t + 4 * x) * p.scale_log2;
             }
         }
-        if constexpr (NT > 1) __syncthreads();
+        if constexpr (NT > 1) __syncwarp();
 
         float m[NT][2], l[NT][2], beta[NT][2];
         float oacc[kMT][NT][4], eights[NT][4];
@@ -371,24 +369,22 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
         const int lo_min = p.window > 0 ? s.len - min(p.window + p.Tq - 1, s.len) : 0;  // first key of the first row
         const int lo_max = p.window > 0 ? s.len - min(p.window, s.len) : -1;  // first key of the last row
 
-        for (int it = 0; it < n_mine; ++it) {
+        for (int it = 0; it < n_tiles; ++it) {
             const bool ready = mbar_wait_bounded(bars + 8 * stage, phase, abort_flag, p.err, p.timeout_ns);
             if (!__all_sync(0xffffffffu, ready)) {
-                // let the copies that are under way land: the later stages, oldest first
-                int st = stage;
-                uint32_t ph = phase;
-                for (int i = it; i < n_mine && i < it + kStages; ++i) {
-                    mbar_wait_drain(bars + 8 * st, ph, p.timeout_ns);
-                    if (++st == kStages) {
-                        st = 0;
-                        ph ^= 1u;
+                // let the copies that are under way land, oldest first
+                for (int i = it; i < n_tiles && i < it + kStages; ++i) {
+                    mbar_wait_drain(bars + 8 * stage, phase, p.timeout_ns);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
                 }
-                break;
+                return;  // no other warp waits for this one
             }
             const uint32_t* K = reinterpret_cast<const uint32_t*>(ring + stage * C::kStage);
             const uint32_t* V = K + C::kTile / 4;
-            const int key0 = key_base + (warp + it * kWarps) * kD4Keys;
+            const int key0 = key_base + it * kKeys;
             // ---- S^T = K Q^T: of each group of 32 keys, accumulator rows g, g + 8 of m16 tile mt are
             // keys 4g + 2mt, 4g + 2mt + 1
             float sacc[U][2][NT][4];
@@ -409,7 +405,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                     if constexpr (NT == 1)
                         f[nt] = qf[i];
                     else
-                        f[nt] = reinterpret_cast<const uint4*>(dec4_smem + C::kQOff)[(i * NT + nt) * 32 + lane];
+                        f[nt] = q_frags[(i * NT + nt) * 32 + lane];
                 }
 #pragma unroll
                 for (int j = 0; j < U; ++j)
@@ -440,7 +436,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                         for (int x = 0; x < 2; ++x)
                             score(j, c, nt, x) = fmaf(score(j, c, nt, x), step, least * sumq[nt][x]);
                 }
-            const bool masked = key0 + kD4Keys > pos_min + 1 || key0 < lo_max;
+            const bool masked = key0 + kKeys > pos_min + 1 || key0 < lo_max;
             if (masked) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -574,15 +570,19 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                 }
             }
             __syncwarp();  // every lane has read the stage
-            if (it + kStages < n_mine) fetch(stage);
+            if (it + kStages < n_tiles) fetch(stage);
             if (++stage == kStages) {
                 stage = 0;
                 phase ^= 1u;
             }
         }
+        if constexpr (NT > 1) __syncwarp();  // every lane has read the Q fragments
 
-        // ---- merge the warps' states, each through its own ring (all its copies are consumed)
-        float* area = reinterpret_cast<float*>(ring);  // m[rows], l[rows], O[rows][D]
+        // ---- the piece's rows: final if it is a whole unit, else partial. A row that sees no key of
+        // the piece: 0, and weight 0 in the merge (NaN stays NaN).
+        const bool whole = t0 == 0 && t1 == s.n;
+        const size_t part = (2 * (size_t)run + (t0 > 0 ? 0 : 1)) * C::kRows;
+        const float down = dec4_pow2(dec4_exponent(top_step) + 10);  // 2^24 / up_step
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -593,94 +593,90 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                     beta[nt][x] += __shfl_xor_sync(0xffffffffu, beta[nt][x], d);
                 }
                 const int n = 8 * nt + 2 * t + x;
-                if (g == 0) {
-                    area[n] = m[nt][x];
-                    area[C::kRows + n] = l[nt][x];
-                }
-                const float down = dec4_pow2(dec4_exponent(top_step) + 10);  // 2^24 / up_step
-                float* out = area + 2 * C::kRows + n * D + 4 * g;
+                if (n >= nrows) continue;
+                const float inv = l[nt][x] == 0.f ? 0.f : 1.f / l[nt][x];
+                if (!whole && g == 0)
+                    p.part_lse[part + n] = l[nt][x] == 0.f ? -INFINITY : m[nt][x] + __log2f(l[nt][x]);
 #pragma unroll
-                for (int i = 0; i < kMT; ++i) {
-                    const float f = i % 2 ? 0.0625f : 1.f;  // odd elements' codes count 16 times
-                    out[64 * (i / 4) + i % 4] = fmaf(fmaf(oacc[i][nt][x], f, -eights[nt][x]), down, beta[nt][x]);
-                    out[64 * (i / 4) + 32 + i % 4] = fmaf(fmaf(oacc[i][nt][x + 2], f, -eights[nt][x]), down, beta[nt][x]);
-                }
-            }
-        __syncthreads();
-        if (*abort_flag) return;  // uniform: the flag is set before the barrier and never cleared
-        const bool whole = t0 == 0 && t1 == s.n;
-        const size_t slot = 2 * (size_t)blockIdx.x + (t0 > 0 ? 0 : 1);
-        for (int idx = threadIdx.x; idx < nrows * D; idx += C::kThreads) {
-            const int row = idx / D, d = idx - row * D;
-            constexpr int kStep = C::kWarpBytes / 4;
-            const float* base = reinterpret_cast<const float*>(dec4_smem);
-            float M = -INFINITY;
+                for (int i = 0; i < kMT / 4; ++i)
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, base[w * kStep + row]);
-            const float mu = M == -INFINITY ? 0.f : M;
-            float sum = 0.f, acc = 0.f;
+                    for (int r = 0; r < 2; ++r) {  // four elements from d = 64i + 32r + 4g
+                        float v[4];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2_approx(base[w * kStep + row] - mu);
-                sum += base[w * kStep + C::kRows + row] * f;
-                acc += base[w * kStep + 2 * C::kRows + row * D + d] * f;
+                        for (int e = 0; e < 4; ++e) {
+                            const float o = oacc[4 * i + e][nt][2 * r + x] * (e % 2 ? 0.0625f : 1.f);  // odd codes count 16 times
+                            v[e] = fmaf(o - eights[nt][x], down, beta[nt][x]) * inv;
+                        }
+                        const int d = 64 * i + 32 * r + 4 * g;
+                        if (whole)
+                            *reinterpret_cast<uint2*>(p.o + (row0 + n) * D + d) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                        else
+                            *reinterpret_cast<float4*>(p.part + (part + n) * D + d) = make_float4(v[0], v[1], v[2], v[3]);
+                    }
             }
-            // a row that sees no key of the piece: 0, and weight 0 in a later merge (NaN stays NaN)
-            const float val = sum == 0.f ? 0.f : acc / sum;
-            if (whole) {
-                p.o[(row0 + row) * D + d] = __float2bfloat16_rn(val);
-            } else {
-                p.part[(slot * C::kRows + row) * D + d] = val;
-                if (d == 0) p.part_lse[slot * C::kRows + row] = sum == 0.f ? -INFINITY : M + __log2f(sum);
-            }
-        }
-        fence_proxy_async_smem();  // the areas are read before the next piece's copies land on them
-        __syncthreads();
     }
 }
 
-// Merge the pieces of the units that were cut between CTAs, in CTA order: one block a unit, one
-// warp a row. The cuts are computed again from the lengths.
+// Merge the pieces of the units that were cut between warps, in run order: one block a row. The
+// cuts follow from the tile counts that the first kernel left.
 template <int D, int NT>
-__global__ void __launch_bounds__(kD4MergeThreads) gqa_decode_kv4_merge_kernel(const Dec4Params p, unsigned grid) {
+__global__ void __launch_bounds__(32 * kD4MergeWarps) gqa_decode_kv4_merge_kernel(const Dec4Params p, unsigned most_runs) {
     constexpr int kRows = 8 * NT;
     constexpr int E = D / 32;
-    constexpr int kWarps = kD4MergeThreads / 32;
-    __shared__ unsigned long long sums[kWarps];
-    const int units = p.Hkv * p.n_rc;
-    const int b = blockIdx.x / units, u = blockIdx.x - b * units;
-    unsigned long long total, before;
-    dec4_sums<kWarps>(
-        p.B, b, sums, [&](int i) { return (unsigned long long)dec4_seq(p, i).n * units; }, &before, &total);
-    const int n = dec4_seq(p, b).n;
+    __shared__ float accs[kD4MergeWarps][D];
+    __shared__ float weights[kD4MergeWarps];
+    const int rows = p.G * p.Tq;  // of a KV head
+    const size_t row = blockIdx.x;
+    const int b = (int)(row / ((size_t)p.Hkv * rows)), in_seq = (int)(row - (size_t)b * p.Hkv * rows);
+    const int h = in_seq / rows, in_group = in_seq - h * rows;
+    const int rc = in_group / kRows, units = p.Hkv * p.n_rc;
+    const unsigned long long start = p.start[b], total = p.start[p.B];
+    const unsigned long long n = (p.start[b + 1] - start) / units;
     if (n == 0) return;
-    const unsigned ctas = (unsigned)min((unsigned long long)grid, total);
-    const unsigned long long first = before + (unsigned long long)u * n, last = first + n - 1;
-    // the CTA of tile w is the last one whose run starts at or before w
-    const unsigned c0 = (unsigned)(((first + 1) * ctas - 1) / total), c1 = (unsigned)(((last + 1) * ctas - 1) / total);
+    const unsigned runs = (unsigned)min((unsigned long long)most_runs, total);
+    const unsigned long long first = start + (unsigned long long)(h * p.n_rc + rc) * n, last = first + n - 1;
+    // the run of tile w is the last one that starts at or before w
+    const unsigned c0 = (unsigned)(((first + 1) * runs - 1) / total), c1 = (unsigned)(((last + 1) * runs - 1) / total);
     if (c0 == c1) return;
-    const int h = u / p.n_rc, rbase = (u - h * p.n_rc) * kRows;
-    const int nrows = min(kRows, p.G * p.Tq - rbase);
-    const int lane = threadIdx.x & 31;
-    for (int row = threadIdx.x >> 5; row < nrows; row += kWarps) {
-        // the first piece starts the unit (slot 1 of its CTA), the others do not (slot 0)
-        const auto at = [&](unsigned c) { return (2 * (size_t)c + (c == c0 ? 1 : 0)) * kRows + row; };
-        float M = -INFINITY;
-        for (unsigned c = c0; c <= c1; ++c) M = fmaxf(M, p.part_lse[at(c)]);
-        const float mu = M == -INFINITY ? 0.f : M;
-        float sum = 0.f, acc[E] = {};
-        for (unsigned c = c0; c <= c1; ++c) {
-            const float f = ex2_approx(p.part_lse[at(c)] - mu);
-            sum += f;
-            const float* src = p.part + at(c) * D + lane * E;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // the first piece starts the unit (slot 1 of its run), the others do not (slot 0)
+    const auto at = [&](unsigned c) { return (2 * (size_t)c + (c == c0 ? 1 : 0)) * kRows + (in_group - rc * kRows); };
+    float M = -INFINITY;
+    for (unsigned c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_lse[at(c)]);
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += f * src[e];
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    if (M == -INFINITY) M = 0.f;
+    float sum = 0.f, acc[E] = {};
+#pragma unroll 4
+    for (unsigned c = c0 + warp; c <= c1; c += kD4MergeWarps) {
+        const float f = ex2_approx(p.part_lse[at(c)] - M);
+        const float* src = p.part + at(c) * D + lane * E;
+        float v[E];
+        if constexpr (E == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src);
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        } else {
+            const float2 x = *reinterpret_cast<const float2*>(src);
+            v[0] = x.x, v[1] = x.y;
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        __nv_bfloat16* out = p.o + (((size_t)b * p.Hq + (size_t)h * p.G) * p.Tq + rbase + row) * D + lane * E;
+        sum += f;
 #pragma unroll
-        for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+        for (int e = 0; e < E; ++e) acc[e] += f * v[e];
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) accs[warp][lane * E + e] = acc[e];
+    if (lane == 0) weights[warp] = sum;
+    __syncthreads();
+    for (int d = 2 * threadIdx.x; d < D; d += 64 * kD4MergeWarps) {
+        float total_weight = 0.f, v[2] = {};
+#pragma unroll
+        for (int w = 0; w < kD4MergeWarps; ++w) {
+            total_weight += weights[w];
+            v[0] += accs[w][d];
+            v[1] += accs[w][d + 1];
+        }
+        const float inv = total_weight == 0.f ? 0.f : 1.f / total_weight;
+        *reinterpret_cast<uint32_t*>(p.o + row * D + d) = pack_bf16x2(v[0] * inv, v[1] * inv);
     }
 }
 

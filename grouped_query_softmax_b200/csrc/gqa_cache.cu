@@ -216,7 +216,7 @@ gqa_status check_dec4(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, i
     if (Tq > kMaxDecodeRows || max_seqlen_k > kDec4MaxKeys) return GQA_ERR_UNSUPPORTED;
     // blocks of the merge in 31 bits; tiles of all units in 52, times the CTAs in 64
     const long long rows = (long long)B * Hq * Tq;
-    if (rows > 0x7fffffffLL || rows * (max_seqlen_k / gqa::kD4Keys + 2) >= 1LL << 52) return GQA_ERR_UNSUPPORTED;
+    if (rows > 0x7fffffffLL || rows * (max_seqlen_k / 32 + 2) >= 1LL << 52) return GQA_ERR_UNSUPPORTED;
     return GQA_OK;
 }
 
@@ -224,36 +224,44 @@ gqa_status check_dec4(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, i
 int dec4_nt(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 struct Dec4Plan {
-    int nt, n_rc, ctas;
+    int nt, n_rc, ctas, warps;  // warps: of a CTA
+    size_t part, lse, start, bytes;  // the workspace's parts and size
 };
-Dec4Plan dec4_plan(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, int window) {
+template <int NT>
+Dec4Plan dec4_plan_nt(int B, int Hkv, int rows, int Tq, int max_seqlen_k, int D, int window) {
+    using C = gqa::Dec4Cfg<128, NT>;  // D changes none of what is used here
     Dec4Plan r;
-    const int rows = Hq / Hkv * Tq;
-    r.nt = dec4_nt(rows);
-    r.n_rc = (rows + 8 * r.nt - 1) / (8 * r.nt);
-    const int per_sm = r.nt == 4 ? 1 : 2, warps = r.nt == 4 ? 8 : 6;  // as Dec4Cfg
-    // no more CTAs than the longest lengths would give a tile for each warp
-    const long long keys = window > 0 ? std::min<long long>(max_seqlen_k, (long long)window + Tq + gqa::kD4Keys) : max_seqlen_k;
-    const long long tiles = (keys + gqa::kD4Keys - 1) / gqa::kD4Keys;
-    const long long most = ((long long)B * Hkv * r.n_rc * tiles + warps - 1) / warps;
-    r.ctas = (int)std::min<long long>((long long)sm_count() * per_sm, most);
+    r.nt = NT;
+    r.n_rc = (rows + C::kRows - 1) / C::kRows;
+    r.warps = C::kWarps;
+    // no more CTAs than the longest lengths have tiles
+    const long long keys = window > 0 ? std::min<long long>(max_seqlen_k, (long long)window + Tq + C::kKeys) : max_seqlen_k;
+    const long long tiles = (long long)B * Hkv * r.n_rc * ((keys + C::kKeys - 1) / C::kKeys);
+    r.ctas = (int)std::min<long long>((long long)sm_count() * C::kCtasPerSm, tiles);
+    const size_t slots = tiles > 1 ? (size_t)2 * r.ctas * r.warps * C::kRows : 0;
+    r.part = 0;
+    r.lse = gqa::round256(slots * D * sizeof(float));
+    r.start = r.lse + gqa::round256(slots * sizeof(float));
+    r.bytes = tiles > 1 ? r.start + ((size_t)B + 1) * sizeof(unsigned long long) : 0;
     return r;
 }
-size_t dec4_lse_offset(const Dec4Plan& r, int D) { return gqa::round256((size_t)2 * r.ctas * 8 * r.nt * D * sizeof(float)); }
-size_t dec4_bytes(const Dec4Plan& r, int D) {
-    return dec4_lse_offset(r, D) + (size_t)2 * r.ctas * 8 * r.nt * sizeof(float);
+Dec4Plan dec4_plan(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, int window) {
+    const int rows = Hq / Hkv * Tq, nt = dec4_nt(rows);
+    return nt == 1   ? dec4_plan_nt<1>(B, Hkv, rows, Tq, max_seqlen_k, D, window)
+           : nt == 2 ? dec4_plan_nt<2>(B, Hkv, rows, Tq, max_seqlen_k, D, window)
+                     : dec4_plan_nt<4>(B, Hkv, rows, Tq, max_seqlen_k, D, window);
 }
 
 template <int D, int NT>
-gqa_status launch_dec4(const gqa::Dec4Params& p, int ctas, cudaStream_t stream) {
+gqa_status launch_dec4(const gqa::Dec4Params& p, const Dec4Plan& r, cudaStream_t stream) {
     using C = gqa::Dec4Cfg<D, NT>;
     cudaError_t e = cudaFuncSetAttribute(gqa::gqa_decode_kv4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::kBytes);
     if (e != cudaSuccess) return GQA_ERR_CUDA;
-    gqa::gqa_decode_kv4_kernel<D, NT><<<(unsigned)ctas, C::kThreads, C::kBytes, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess || ctas == 1) return launched(e);
-    gqa::gqa_decode_kv4_merge_kernel<D, NT>
-        <<<(unsigned)(p.B * p.Hkv * p.n_rc), gqa::kD4MergeThreads, 0, stream>>>(p, (unsigned)ctas);
+    gqa::gqa_decode_kv4_kernel<D, NT><<<(unsigned)r.ctas, C::kThreads, C::kBytes, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess || r.bytes == 0) return launched(e);
+    gqa::gqa_decode_kv4_merge_kernel<D, NT><<<(unsigned)(p.B * p.Hq * p.Tq), 32 * gqa::kD4MergeWarps, 0, stream>>>(
+        p, (unsigned)(r.ctas * r.warps));
     return launched(cudaGetLastError());
 }
 
@@ -428,8 +436,7 @@ gqa_status gqa_kv4_gather(const void* k_pool, const void* v_pool, void* k, void*
 
 size_t gqa_attn_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, int window) {
     if (check_dec4(B, Hq, Hkv, Tq, max_seqlen_k, D, window) != GQA_OK) return 0;
-    const Dec4Plan r = dec4_plan(B, Hq, Hkv, Tq, max_seqlen_k, D, window);
-    return r.ctas == 1 ? 0 : dec4_bytes(r, D);
+    return dec4_plan(B, Hq, Hkv, Tq, max_seqlen_k, D, window).bytes;
 }
 
 gqa_status gqa_attn_decode_kv4(const void* q, const void* k_pool, const void* v_pool, void* o, const int* seqlens_k,
@@ -447,10 +454,12 @@ gqa_status gqa_attn_decode_kv4(const void* q, const void* k_pool, const void* v_
     if ((st = check_kv4_pool(k_pool, k_layout, num_pages, Hkv, page_size, D, &p.k_sb, &p.k_sh)) != GQA_OK) return st;
     if ((st = check_kv4_pool(v_pool, v_layout, num_pages, Hkv, page_size, D, &p.v_sb, &p.v_sh)) != GQA_OK) return st;
     const Dec4Plan r = dec4_plan(B, Hq, Hkv, Tq, max_seqlen_k, D, window);
-    if (r.ctas > 1) {
-        if (!aligned(workspace, 256) || workspace_bytes < dec4_bytes(r, D)) return GQA_ERR_WORKSPACE;
-        p.part = static_cast<float*>(workspace);
-        p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + dec4_lse_offset(r, D));
+    if (r.bytes > 0) {
+        if (!aligned(workspace, 256) || workspace_bytes < r.bytes) return GQA_ERR_WORKSPACE;
+        char* ws = static_cast<char*>(workspace);
+        p.part = reinterpret_cast<float*>(ws + r.part);
+        p.part_lse = reinterpret_cast<float*>(ws + r.lse);
+        p.start = reinterpret_cast<unsigned long long*>(ws + r.start);
     }
     p.q = static_cast<const bf16*>(q);
     p.o = static_cast<bf16*>(o);
@@ -474,12 +483,12 @@ gqa_status gqa_attn_decode_kv4(const void* q, const void* k_pool, const void* v_
     if ((p.err = gqa::device_error_ptr()) == nullptr) return GQA_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (D == 128)
-        return r.nt == 1   ? launch_dec4<128, 1>(p, r.ctas, s)
-               : r.nt == 2 ? launch_dec4<128, 2>(p, r.ctas, s)
-                           : launch_dec4<128, 4>(p, r.ctas, s);
-    return r.nt == 1   ? launch_dec4<64, 1>(p, r.ctas, s)
-           : r.nt == 2 ? launch_dec4<64, 2>(p, r.ctas, s)
-                       : launch_dec4<64, 4>(p, r.ctas, s);
+        return r.nt == 1   ? launch_dec4<128, 1>(p, r, s)
+               : r.nt == 2 ? launch_dec4<128, 2>(p, r, s)
+                           : launch_dec4<128, 4>(p, r, s);
+    return r.nt == 1   ? launch_dec4<64, 1>(p, r, s)
+           : r.nt == 2 ? launch_dec4<64, 2>(p, r, s)
+                       : launch_dec4<64, 4>(p, r, s);
 }
 
 }  // extern "C"

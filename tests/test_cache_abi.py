@@ -144,10 +144,10 @@ def test_decode_rejects_bad_arguments(gqa, kw, status):
 
 
 def test_workspace_sizes(gqa):
-    # one CTA needs none; more need two partial states of a CTA's rows, D floats and a log-sum-exp each
-    assert gqa.gqa_attn_decode_kv4_workspace_bytes(1, 4, 2, 1, 32, 128) == 0
+    assert gqa.gqa_attn_decode_kv4_workspace_bytes(1, 4, 1, 1, 32, 128) == 0  # a single tile is never cut
     n = gqa.gqa_attn_decode_kv4_workspace_bytes(1, 8, 8, 1, 1024, 128)
-    assert n > 0 and n % (2 * 8 * (128 + 1) * 4) == 0  # two partial states of 8 rows a CTA
+    assert n > 0  # partial states of the units that are cut
+    assert n < gqa.gqa_attn_decode_kv4_workspace_bytes(1, 8, 8, 1, 32768, 128) <= 64 << 20
     assert gqa.gqa_attn_decode_kv4_workspace_bytes(1, 8, 8, 17, 1024, 128) == 0
     assert gqa.gqa_qk_norm_rope_bwd_workspace_bytes(1, 16, 8, 2, 128) % 256 == 0
     assert gqa.gqa_qk_norm_rope_bwd_workspace_bytes(1, 16, 8, 3, 128) == 0
