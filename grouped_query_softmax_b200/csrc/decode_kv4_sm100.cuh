@@ -50,7 +50,7 @@ struct Dec4Params {
     float scale_log2;
     float* part;      // [2 * warps, rows, D] partial outputs
     float* part_lse;  // [2 * warps, rows] log2-domain log-sum-exp
-    unsigned long long* start;  // [B + 1] tiles before each sequence, and all of them
+    int2* ends;       // [B * Hkv * n_rc] first and last run of each unit's pieces
     uint32_t* err;
     unsigned long long timeout_ns;
 };
@@ -59,11 +59,12 @@ template <int D, int NT>
 struct Dec4Cfg {
     static constexpr int kRows = 8 * NT;                // query rows a warp takes
     static constexpr int kRow = D / 2 + 4;              // bytes of a stored row
-    static constexpr int kGroups = NT == 1 ? 2 : 1;     // groups of 32 keys (two m16 tiles) in a tile
+    // groups of 32 keys (two m16 tiles) in a tile: two, where the registers hold their scores
+    static constexpr int kGroups = NT * D <= 128 ? 2 : 1;
     static constexpr int kKeys = 32 * kGroups;
     static constexpr int kTile = kKeys * kRow;          // K or V rows of a tile
     static constexpr int kStage = 2 * kTile;
-    static constexpr int kStages = NT == 1 ? 2 : NT == 2 ? 3 : 4;
+    static constexpr int kStages = NT * D <= 128 ? 2 : NT == 4 ? 4 : 3;
     static constexpr int kWarps = NT == 4 ? 8 : 6;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kCtasPerSm = NT == 4 ? 1 : 2;
@@ -208,13 +209,9 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                 ctl->first[w] = lo;
             }
         }
-        if (blockIdx.x == 0 && b < p.B) {
-            if (p.start != nullptr) p.start[b] = lo;
-            if (x == 0) atomicOr(p.err, kDevErrBadSeqlens);
-        }
+        if (blockIdx.x == 0 && b < p.B && x == 0) atomicOr(p.err, kDevErrBadSeqlens);
         __syncthreads();
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0 && p.start != nullptr) p.start[p.B] = total;
     if (run >= runs) return;
     unsigned long long at = dec4_cut(total, run, runs);
     const unsigned long long end = dec4_cut(total, run + 1, runs);
@@ -582,6 +579,11 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
         // the piece: 0, and weight 0 in the merge (NaN stays NaN).
         const bool whole = t0 == 0 && t1 == s.n;
         const size_t part = (2 * (size_t)run + (t0 > 0 ? 0 : 1)) * C::kRows;
+        if (lane == 0 && p.ends != nullptr) {
+            int2* e = p.ends + (size_t)b * units + u;
+            if (t0 == 0) e->x = (int)run;
+            if (t1 == s.n) e->y = (int)run;
+        }
         const float down = dec4_pow2(dec4_exponent(top_step) + 10);  // 2^24 / up_step
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -617,38 +619,33 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
     }
 }
 
-// Merge the pieces of the units that were cut between warps, in run order: one block a row. The
-// cuts follow from the tile counts that the first kernel left.
+// Merge the pieces of the units that were cut between warps, in run order: one block a row, of
+// sequence blockIdx.x. Which runs they are the first kernel has left.
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kD4MergeWarps) gqa_decode_kv4_merge_kernel(const Dec4Params p, unsigned most_runs) {
+__global__ void __launch_bounds__(32 * kD4MergeWarps) gqa_decode_kv4_merge_kernel(const Dec4Params p) {
     constexpr int kRows = 8 * NT;
     constexpr int E = D / 32;
     __shared__ float accs[kD4MergeWarps][D];
     __shared__ float weights[kD4MergeWarps];
     const int rows = p.G * p.Tq;  // of a KV head
-    const size_t row = blockIdx.x;
-    const int b = (int)(row / ((size_t)p.Hkv * rows)), in_seq = (int)(row - (size_t)b * p.Hkv * rows);
-    const int h = in_seq / rows, in_group = in_seq - h * rows;
-    const int rc = in_group / kRows, units = p.Hkv * p.n_rc;
-    const unsigned long long start = p.start[b], total = p.start[p.B];
-    const unsigned long long n = (p.start[b + 1] - start) / units;
-    if (n == 0) return;
-    const unsigned runs = (unsigned)min((unsigned long long)most_runs, total);
-    const unsigned long long first = start + (unsigned long long)(h * p.n_rc + rc) * n, last = first + n - 1;
-    // the run of tile w is the last one that starts at or before w
-    const unsigned c0 = (unsigned)(((first + 1) * runs - 1) / total), c1 = (unsigned)(((last + 1) * runs - 1) / total);
-    if (c0 == c1) return;
+    const int h = (int)blockIdx.y / rows, in_group = (int)blockIdx.y - h * rows;
+    const int rc = in_group / kRows;
+    const int2 ends = p.ends[((size_t)blockIdx.x * p.Hkv + h) * p.n_rc + rc];
+    const int len = __ldg(p.seqlens + blockIdx.x);
+    if (len < 0 || len > p.capacity || ends.x == ends.y) return;  // no output, or whole
+    const size_t row = (size_t)blockIdx.x * gridDim.y + blockIdx.y;
+    const int c0 = ends.x, c1 = ends.y;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // the first piece starts the unit (slot 1 of its run), the others do not (slot 0)
-    const auto at = [&](unsigned c) { return (2 * (size_t)c + (c == c0 ? 1 : 0)) * kRows + (in_group - rc * kRows); };
+    const auto at = [&](int c) { return (2 * (size_t)c + (c == c0 ? 1 : 0)) * kRows + (in_group - rc * kRows); };
     float M = -INFINITY;
-    for (unsigned c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_lse[at(c)]);
+    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_lse[at(c)]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
     if (M == -INFINITY) M = 0.f;
     float sum = 0.f, acc[E] = {};
 #pragma unroll 4
-    for (unsigned c = c0 + warp; c <= c1; c += kD4MergeWarps) {
+    for (int c = c0 + warp; c <= c1; c += kD4MergeWarps) {
         const float f = ex2_approx(p.part_lse[at(c)] - M);
         const float* src = p.part + at(c) * D + lane * E;
         float v[E];

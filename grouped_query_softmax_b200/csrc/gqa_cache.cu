@@ -214,9 +214,9 @@ gqa_status check_dec4(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, i
     if (st != GQA_OK) return st;
     if (B <= 0 || Tq <= 0 || max_seqlen_k <= 0 || window < 0) return GQA_ERR_INVALID_ARGUMENT;
     if (Tq > kMaxDecodeRows || max_seqlen_k > kDec4MaxKeys) return GQA_ERR_UNSUPPORTED;
-    // blocks of the merge in 31 bits; tiles of all units in 52, times the CTAs in 64
+    // the merge's grid; tiles of all units in 52 bits, times the warps in 64
     const long long rows = (long long)B * Hq * Tq;
-    if (rows > 0x7fffffffLL || rows * (max_seqlen_k / 32 + 2) >= 1LL << 52) return GQA_ERR_UNSUPPORTED;
+    if ((long long)Hq * Tq > 65535 || rows > 0x7fffffffLL || rows * (max_seqlen_k / 32 + 2) >= 1LL << 52) return GQA_ERR_UNSUPPORTED;
     return GQA_OK;
 }
 
@@ -225,11 +225,11 @@ int dec4_nt(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 struct Dec4Plan {
     int nt, n_rc, ctas, warps;  // warps: of a CTA
-    size_t part, lse, start, bytes;  // the workspace's parts and size
+    size_t part, lse, ends, bytes;  // the workspace's parts and size
 };
-template <int NT>
-Dec4Plan dec4_plan_nt(int B, int Hkv, int rows, int Tq, int max_seqlen_k, int D, int window) {
-    using C = gqa::Dec4Cfg<128, NT>;  // D changes none of what is used here
+template <int D, int NT>
+Dec4Plan dec4_plan_for(int B, int Hkv, int rows, int Tq, int max_seqlen_k, int window) {
+    using C = gqa::Dec4Cfg<D, NT>;
     Dec4Plan r;
     r.nt = NT;
     r.n_rc = (rows + C::kRows - 1) / C::kRows;
@@ -241,15 +241,19 @@ Dec4Plan dec4_plan_nt(int B, int Hkv, int rows, int Tq, int max_seqlen_k, int D,
     const size_t slots = tiles > 1 ? (size_t)2 * r.ctas * r.warps * C::kRows : 0;
     r.part = 0;
     r.lse = gqa::round256(slots * D * sizeof(float));
-    r.start = r.lse + gqa::round256(slots * sizeof(float));
-    r.bytes = tiles > 1 ? r.start + ((size_t)B + 1) * sizeof(unsigned long long) : 0;
+    r.ends = r.lse + gqa::round256(slots * sizeof(float));
+    r.bytes = tiles > 1 ? r.ends + (size_t)B * Hkv * r.n_rc * sizeof(int2) : 0;
     return r;
 }
 Dec4Plan dec4_plan(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, int window) {
     const int rows = Hq / Hkv * Tq, nt = dec4_nt(rows);
-    return nt == 1   ? dec4_plan_nt<1>(B, Hkv, rows, Tq, max_seqlen_k, D, window)
-           : nt == 2 ? dec4_plan_nt<2>(B, Hkv, rows, Tq, max_seqlen_k, D, window)
-                     : dec4_plan_nt<4>(B, Hkv, rows, Tq, max_seqlen_k, D, window);
+    if (D == 128)
+        return nt == 1   ? dec4_plan_for<128, 1>(B, Hkv, rows, Tq, max_seqlen_k, window)
+               : nt == 2 ? dec4_plan_for<128, 2>(B, Hkv, rows, Tq, max_seqlen_k, window)
+                         : dec4_plan_for<128, 4>(B, Hkv, rows, Tq, max_seqlen_k, window);
+    return nt == 1   ? dec4_plan_for<64, 1>(B, Hkv, rows, Tq, max_seqlen_k, window)
+           : nt == 2 ? dec4_plan_for<64, 2>(B, Hkv, rows, Tq, max_seqlen_k, window)
+                     : dec4_plan_for<64, 4>(B, Hkv, rows, Tq, max_seqlen_k, window);
 }
 
 template <int D, int NT>
@@ -260,8 +264,8 @@ gqa_status launch_dec4(const gqa::Dec4Params& p, const Dec4Plan& r, cudaStream_t
     if (e != cudaSuccess) return GQA_ERR_CUDA;
     gqa::gqa_decode_kv4_kernel<D, NT><<<(unsigned)r.ctas, C::kThreads, C::kBytes, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess || r.bytes == 0) return launched(e);
-    gqa::gqa_decode_kv4_merge_kernel<D, NT><<<(unsigned)(p.B * p.Hq * p.Tq), 32 * gqa::kD4MergeWarps, 0, stream>>>(
-        p, (unsigned)(r.ctas * r.warps));
+    const dim3 grid((unsigned)p.B, (unsigned)(p.Hq * p.Tq));
+    gqa::gqa_decode_kv4_merge_kernel<D, NT><<<grid, 32 * gqa::kD4MergeWarps, 0, stream>>>(p);
     return launched(cudaGetLastError());
 }
 
@@ -459,7 +463,7 @@ gqa_status gqa_attn_decode_kv4(const void* q, const void* k_pool, const void* v_
         char* ws = static_cast<char*>(workspace);
         p.part = reinterpret_cast<float*>(ws + r.part);
         p.part_lse = reinterpret_cast<float*>(ws + r.lse);
-        p.start = reinterpret_cast<unsigned long long*>(ws + r.start);
+        p.ends = reinterpret_cast<int2*>(ws + r.ends);
     }
     p.q = static_cast<const bf16*>(q);
     p.o = static_cast<bf16*>(o);
