@@ -66,8 +66,7 @@ gqa_status rope_params(gqa::RopeParams& p, const gqa_rope* r, int B, int T, int 
     p.x[0].weight = r->q_weight;
     p.x[1].weight = r->k_weight;
     p.weight_fp32 = r->weight_fp32 != 0;
-    if (!aligned_or_null(r->q_weight, p.weight_fp32 ? 4 : 2) || !aligned_or_null(r->k_weight, p.weight_fp32 ? 4 : 2))
-        return GQA_ERR_INVALID_ARGUMENT;
+    if (!aligned_or_null(r->q_weight, 16) || !aligned_or_null(r->k_weight, 16)) return GQA_ERR_INVALID_ARGUMENT;
     if (!(r->eps >= 0.f) || std::isinf(r->eps)) return GQA_ERR_INVALID_ARGUMENT;
     p.eps = r->eps;
     if ((r->cos == nullptr) != (r->sin == nullptr)) return GQA_ERR_INVALID_ARGUMENT;
@@ -92,58 +91,65 @@ gqa_status rope_params(gqa::RopeParams& p, const gqa_rope* r, int B, int T, int 
     return GQA_OK;
 }
 
-// Heads of a token that one team of D/8 lanes takes in turn: all its loads of the angles and
-// weights serve that many rows, so a large launch takes many; a small one takes few, to spread
-// over the SMs.
+// Heads of a token that one team of D/8 lanes takes in turn: its loads of the angles and weights
+// serve that many rows, so a large launch takes many; a small one takes the four it has in
+// flight at a time, to spread over the SMs.
 int rope_heads_per_team(long long tokens, int heads, int D, int sms) {
-    const long long teams_at_8 = tokens * ((heads + 7) / 8);
-    return teams_at_8 * (D / 8) >= (long long)sms * 2048 ? 8 : 4;
+    const long long lanes_at_16 = tokens * ((heads + 15) / 16) * (D / 8);
+    return lanes_at_16 >= (long long)sms * 2048 ? 16 : gqa::kRopeUnroll;
+}
+// Heads, split into blocks; false if there are more blocks than a grid's y extent.
+bool rope_blocks(gqa::RopeParams& p, int heads_per_team) {
+    p.heads_per_team = heads_per_team;
+    int all = 0;
+    for (int i = 0; i < 3; ++i) all += p.blocks[i] = (p.x[i].H + heads_per_team - 1) / heads_per_team;
+    return all <= 65535;
 }
 
 template <int D>
 gqa_status rope_fwd(gqa::RopeParams p, bool interleaved, cudaStream_t stream) {
+    int heads = 0;
+    for (int i = 0; i < 3; ++i) heads += p.x[i].H;
+    if (!rope_blocks(p, rope_heads_per_team((long long)p.B * p.T, heads, D, sm_count()))) return GQA_ERR_UNSUPPORTED;
     if ((p.err = gqa::device_error_ptr()) == nullptr) return GQA_ERR_CUDA;
-    const long long teams = (long long)p.B * p.T * (p.blocks[0] + p.blocks[1] + p.blocks[2]);
     constexpr int kPer = gqa::kRopeThreads / (D / 8);
-    const long long ctas = (teams + kPer - 1) / kPer;
-    if (ctas > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)(((long long)p.B * p.T + kPer - 1) / kPer), (unsigned)(p.blocks[0] + p.blocks[1] + p.blocks[2]));
     if (interleaved)
-        gqa::gqa_rope_fwd_kernel<D, true><<<(unsigned)ctas, gqa::kRopeThreads, 0, stream>>>(p);
+        gqa::gqa_rope_fwd_kernel<D, true><<<grid, gqa::kRopeThreads, 0, stream>>>(p);
     else
-        gqa::gqa_rope_fwd_kernel<D, false><<<(unsigned)ctas, gqa::kRopeThreads, 0, stream>>>(p);
+        gqa::gqa_rope_fwd_kernel<D, false><<<grid, gqa::kRopeThreads, 0, stream>>>(p);
     return launched(cudaGetLastError());
 }
 
-// CTAs of the backward pass: queries' first, then keys'. Each leaves one row of weight sums.
+// The backward pass's CTAs: a head block each, over tokens in strides of the grid's x extent, at most
+// eight a SM. Each leaves one row of weight sums.
 struct RopeBwdPlan {
-    int heads_per_team, q_ctas, k_ctas;
+    int heads_per_team, blocks, x;
 };
 RopeBwdPlan rope_bwd_plan(int B, int T, int Hq, int Hkv, int D) {
-    const int sms = sm_count();
+    const int sms = sm_count(), per_cta = gqa::kRopeThreads / (D / 8);
+    const long long tokens = (long long)B * T;
     RopeBwdPlan r;
-    r.heads_per_team = rope_heads_per_team((long long)B * T, Hq + Hkv, D, sms);
-    const int per_cta = gqa::kRopeThreads / (D / 8);
-    const auto ctas = [&](int H) {
-        const long long units = (long long)B * T * ((H + r.heads_per_team - 1) / r.heads_per_team);
-        const long long most = std::max<long long>(1, (long long)sms * 8 * H / (Hq + Hkv));
-        return (int)std::min<long long>((units + per_cta - 1) / per_cta, most);
-    };
-    r.q_ctas = ctas(Hq);
-    r.k_ctas = ctas(Hkv);
+    r.heads_per_team = rope_heads_per_team(tokens, Hq + Hkv, D, sms);
+    r.blocks = (Hq + r.heads_per_team - 1) / r.heads_per_team + (Hkv + r.heads_per_team - 1) / r.heads_per_team;
+    r.x = (int)std::min<long long>((tokens + per_cta - 1) / per_cta, std::max(1, sms * 8 / r.blocks));
     return r;
 }
 
 template <int D>
-gqa_status rope_bwd(gqa::RopeParams p, int ctas, bool interleaved, float* dq_weight, float* dk_weight,
+gqa_status rope_bwd(gqa::RopeParams p, const RopeBwdPlan& r, bool interleaved, float* dq_weight, float* dk_weight,
                     cudaStream_t stream) {
+    if (!rope_blocks(p, r.heads_per_team)) return GQA_ERR_UNSUPPORTED;
     if ((p.err = gqa::device_error_ptr()) == nullptr) return GQA_ERR_CUDA;
+    const dim3 grid((unsigned)r.x, (unsigned)r.blocks);
     if (interleaved)
-        gqa::gqa_rope_bwd_kernel<D, true><<<(unsigned)ctas, gqa::kRopeThreads, 0, stream>>>(p);
+        gqa::gqa_rope_bwd_kernel<D, true><<<grid, gqa::kRopeThreads, 0, stream>>>(p);
     else
-        gqa::gqa_rope_bwd_kernel<D, false><<<(unsigned)ctas, gqa::kRopeThreads, 0, stream>>>(p);
+        gqa::gqa_rope_bwd_kernel<D, false><<<grid, gqa::kRopeThreads, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (dq_weight == nullptr && dk_weight == nullptr)) return launched(e);
-    gqa::gqa_rope_dw_kernel<D><<<2, 1024, 0, stream>>>(p.partial, p.q_blocks, ctas, dq_weight, dk_weight);
+    gqa::gqa_rope_dw_kernel<D><<<dim3(2, D / 32), 1024, 0, stream>>>(p.partial, p.blocks[0] * r.x, r.blocks * r.x, dq_weight,
+                                                                     dk_weight);
     return launched(cudaGetLastError());
 }
 
@@ -325,9 +331,6 @@ gqa_status gqa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_o
     y.in = static_cast<const bf16*>(k);
     x.out = static_cast<bf16*>(q_out);
     y.out = static_cast<bf16*>(k_out);
-    p.heads_per_team = rope_heads_per_team((long long)B * T, Hq + Hkv, D, sm_count());
-    p.blocks[0] = (Hq + p.heads_per_team - 1) / p.heads_per_team;
-    p.blocks[1] = (Hkv + p.heads_per_team - 1) / p.heads_per_team;
     const bool inter = rope->interleaved != 0;
     return D == 128 ? rope_fwd<128>(p, inter, static_cast<cudaStream_t>(stream))
                     : rope_fwd<64>(p, inter, static_cast<cudaStream_t>(stream));
@@ -364,9 +367,6 @@ gqa_status gqa_qk_norm_rope_append(const void* q, const void* k, const void* v, 
     p.slots = slots;
     p.page_size = page_size;
     p.num_pages = num_pages;
-    p.heads_per_team = rope_heads_per_team(N, Hq + 2 * Hkv, D, sm_count());
-    p.blocks[0] = (Hq + p.heads_per_team - 1) / p.heads_per_team;
-    p.blocks[1] = p.blocks[2] = (Hkv + p.heads_per_team - 1) / p.heads_per_team;
     const bool inter = rope->interleaved != 0;
     return D == 128 ? rope_fwd<128>(p, inter, static_cast<cudaStream_t>(stream))
                     : rope_fwd<64>(p, inter, static_cast<cudaStream_t>(stream));
@@ -375,7 +375,7 @@ gqa_status gqa_qk_norm_rope_append(const void* q, const void* k, const void* v, 
 size_t gqa_qk_norm_rope_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
     if (check_heads(Hq, Hkv, D) != GQA_OK || B <= 0 || T <= 0) return 0;
     const RopeBwdPlan r = rope_bwd_plan(B, T, Hq, Hkv, D);
-    return gqa::round256((size_t)(r.q_ctas + r.k_ctas) * D * sizeof(float));
+    return gqa::round256((size_t)r.blocks * r.x * D * sizeof(float));
 }
 
 gqa_status gqa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, void* dq, void* dk,
@@ -413,14 +413,9 @@ gqa_status gqa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const vo
     y.in = static_cast<const bf16*>(k);
     x.out = static_cast<bf16*>(dq);
     y.out = static_cast<bf16*>(dk);
-    p.heads_per_team = r.heads_per_team;
-    p.blocks[0] = (Hq + r.heads_per_team - 1) / r.heads_per_team;
-    p.blocks[1] = (Hkv + r.heads_per_team - 1) / r.heads_per_team;
-    p.q_blocks = r.q_ctas;
-    const int ctas = r.q_ctas + r.k_ctas;
     const bool inter = rope->interleaved != 0;
-    return D == 128 ? rope_bwd<128>(p, ctas, inter, dq_weight, dk_weight, static_cast<cudaStream_t>(stream))
-                    : rope_bwd<64>(p, ctas, inter, dq_weight, dk_weight, static_cast<cudaStream_t>(stream));
+    return D == 128 ? rope_bwd<128>(p, r, inter, dq_weight, dk_weight, static_cast<cudaStream_t>(stream))
+                    : rope_bwd<64>(p, r, inter, dq_weight, dk_weight, static_cast<cudaStream_t>(stream));
 }
 
 gqa_status gqa_kv4_append(const void* k, const void* v, void* k_pool, void* v_pool, const int* slots, int N, int Hkv,

@@ -12,11 +12,14 @@
 //   dw = sum over rows of g * n,   dx = rsqrt(...) * (e - n * mean(e * n)).
 // n is computed again from x, which costs a read that the pass makes anyway.
 //
-// All of it is bound by HBM: a row is read once and written once (backward: two reads). D/8
-// lanes take a row, each lane eight elements in two groups of four that hold whole pairs, so
-// the rotation needs no exchange and the row's sum is D/8-lane shuffles. A lane keeps its cos,
-// sin and weights in registers over the heads of one token. Everything between the loads and
-// the one rounding to bf16 at the end is fp32.
+// All of it is bound by HBM: a row is read once and written once (backward: two reads). What has to
+// be kept small beside it is instructions. D/8 lanes take a row, each lane eight elements in two
+// groups of four that hold whole pairs, so the rotation needs no exchange, and packed pairs of
+// fp32 do the arithmetic. A lane keeps its angles and weights in registers over the heads of a
+// token, four rows at a time: their sums over the lanes are formed together, each step of the
+// exchange halving the rows that a lane still adds up, so four rows cost five exchanges and one
+// reciprocal root instead of sixteen and four. Everything between the loads and the one rounding
+// to bf16 at the end is fp32.
 #pragma once
 
 #include "sm100_ptx.cuh"
@@ -37,6 +40,8 @@ struct RopeRows {
     int H;
 };
 
+constexpr int kRopeUnroll = 4;  // rows a team takes at a time
+
 struct RopeParams {
     RopeRows x[3];       // queries, keys, values (values only when appending; copied)
     const float* cos;    // [n_positions, rot/2] or null
@@ -52,9 +57,8 @@ struct RopeParams {
     const int* slots;  // [T], or null: not appending
     int page_size, num_pages;
     int heads_per_team;  // rows of one token that a team takes in turn
-    int blocks[3];       // head blocks of each operand
-    float* partial;      // backward: [gridDim.x, D] sums of dw, queries' blocks first
-    int q_blocks;        // backward: CTAs that take queries
+    int blocks[3];       // head blocks of each operand; gridDim.y is their sum
+    float* partial;      // backward: [gridDim.y, gridDim.x, D] sums of dw
     uint32_t* err;
 };
 
@@ -85,145 +89,246 @@ __device__ __forceinline__ RopeLane rope_lane(int j, int rot) {
     return l;
 }
 
-__device__ __forceinline__ void rope_unpack(uint2 u, float* f) {
-    f[0] = __uint_as_float(u.x << 16);
-    f[1] = __uint_as_float(u.x & 0xffff0000u);
-    f[2] = __uint_as_float(u.y << 16);
-    f[3] = __uint_as_float(u.y & 0xffff0000u);
+// Two fp32 values in one register pair.
+__device__ __forceinline__ uint64_t rope2(float lo, float hi) { return f2_pack(lo, hi); }
+__device__ __forceinline__ uint64_t rope2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
-__device__ __forceinline__ uint2 rope_pack(const float* f) {
-    return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+__device__ __forceinline__ uint64_t rope2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ float rope2_sum(uint64_t a) {
+    float lo, hi;
+    f2_unpack(a, lo, hi);
+    return lo + hi;
+}
+__device__ __forceinline__ uint64_t rope2_neg(uint64_t a) { return a ^ 0x8000000080000000ull; }
+
+// A lane's eight elements as the first and second elements of its four pairs, two pairs a register.
+struct RopePairs {
+    uint64_t a[2], b[2];
+};
+__device__ __forceinline__ uint64_t rope_lows(uint32_t u, uint32_t v) {
+    return rope2(__uint_as_float(u << 16), __uint_as_float(v << 16));
+}
+__device__ __forceinline__ uint64_t rope_highs(uint32_t u, uint32_t v) {
+    return rope2(__uint_as_float(u & 0xffff0000u), __uint_as_float(v & 0xffff0000u));
+}
+__device__ __forceinline__ uint64_t rope_both(uint32_t u) {
+    return rope2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t rope_round(uint64_t v) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return pack_bf16x2(lo, hi);
+}
+template <bool kInterleaved>
+__device__ __forceinline__ RopePairs rope_unpack(uint2 u0, uint2 u1) {
+    RopePairs p;
+    if (kInterleaved) {
+        p.a[0] = rope_lows(u0.x, u0.y), p.b[0] = rope_highs(u0.x, u0.y);
+        p.a[1] = rope_lows(u1.x, u1.y), p.b[1] = rope_highs(u1.x, u1.y);
+    } else {
+        p.a[0] = rope_both(u0.x), p.a[1] = rope_both(u0.y);
+        p.b[0] = rope_both(u1.x), p.b[1] = rope_both(u1.y);
+    }
+    return p;
+}
+template <bool kInterleaved>
+__device__ __forceinline__ void rope_pack(const RopePairs& p, uint2& u0, uint2& u1) {
+    if (kInterleaved) {
+        float a0, a1, b0, b1;
+        f2_unpack(p.a[0], a0, a1);
+        f2_unpack(p.b[0], b0, b1);
+        u0 = make_uint2(pack_bf16x2(a0, b0), pack_bf16x2(a1, b1));
+        f2_unpack(p.a[1], a0, a1);
+        f2_unpack(p.b[1], b0, b1);
+        u1 = make_uint2(pack_bf16x2(a0, b0), pack_bf16x2(a1, b1));
+    } else {
+        u0 = make_uint2(rope_round(p.a[0]), rope_round(p.a[1]));
+        u1 = make_uint2(rope_round(p.b[0]), rope_round(p.b[1]));
+    }
 }
 __device__ __forceinline__ uint2 rope_load(const __nv_bfloat16* p) { return __ldcs(reinterpret_cast<const uint2*>(p)); }
 
-__device__ __forceinline__ void rope_weight(const void* w, int fp32, int e, float* f) {
-    if (fp32) {
-        for (int i = 0; i < 4; ++i) f[i] = static_cast<const float*>(w)[e + i];
-    } else {
-        for (int i = 0; i < 4; ++i) f[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(w)[e + i]);
-    }
-}
-
-// Turn the eight elements' pairs by +angle (dir = 1) or -angle (dir = -1).
+// A lane's weights in the order of its pairs (without a weight: ones).
 template <bool kInterleaved>
-__device__ __forceinline__ void rope_turn(float* a, float* b, const float4& c, const float4& s, float dir) {
-    const float cs[4] = {c.x, c.y, c.z, c.w};
-    const float sn[4] = {s.x * dir, s.y * dir, s.z * dir, s.w * dir};
-    if (kInterleaved) {
+__device__ __forceinline__ RopePairs rope_weights(const void* w, int fp32, const RopeLane& l) {
+    float f[8];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
-            a[2 * i] = a0 * cs[i] - a1 * sn[i];
-            a[2 * i + 1] = a1 * cs[i] + a0 * sn[i];
-            b[2 * i] = b0 * cs[2 + i] - b1 * sn[2 + i];
-            b[2 * i + 1] = b1 * cs[2 + i] + b0 * sn[2 + i];
-        }
-    } else {
+    for (int i = 0; i < 8; ++i) f[i] = 1.f;
+    if (w != nullptr && fp32) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + l.e0));
+        const float4 y = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + l.e1));
+        f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w, f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
+    } else if (w != nullptr) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + l.e0));
+        const uint2 y = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + l.e1));
+        const uint32_t u[4] = {x.x, x.y, y.x, y.y};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float x = a[i], y = b[i];
-            a[i] = x * cs[i] - y * sn[i];
-            b[i] = y * cs[i] + x * sn[i];
-        }
+        for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(u[i] << 16), f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
+    RopePairs p;
+    if (kInterleaved) {
+        p.a[0] = rope2(f[0], f[2]), p.b[0] = rope2(f[1], f[3]);
+        p.a[1] = rope2(f[4], f[6]), p.b[1] = rope2(f[5], f[7]);
+    } else {
+        p.a[0] = rope2(f[0], f[1]), p.a[1] = rope2(f[2], f[3]);
+        p.b[0] = rope2(f[4], f[5]), p.b[1] = rope2(f[6], f[7]);
+    }
+    return p;
 }
 
+// Sums of four rows' values over the team's lanes: lane j ends with the sum of row rope_row(j).
 template <int kLanes>
-__device__ __forceinline__ float rope_team_sum(float v) {
+__device__ __forceinline__ int rope_row(int j) {
+    return (j & (kLanes / 2) ? 1 : 0) + (j & (kLanes / 4) ? 2 : 0);
+}
+template <int kLanes>
+__device__ __forceinline__ float rope_sums(const float (&v)[4], int j) {
+    const bool h = j & (kLanes / 2), q = j & (kLanes / 4);
+    const float t0 = (h ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, h ? v[0] : v[1], kLanes / 2);
+    const float t1 = (h ? v[3] : v[2]) + __shfl_xor_sync(0xffffffffu, h ? v[2] : v[3], kLanes / 2);
+    float s = (q ? t1 : t0) + __shfl_xor_sync(0xffffffffu, q ? t0 : t1, kLanes / 4);
 #pragma unroll
-    for (int d = kLanes / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d, kLanes);
-    return v;
+    for (int d = kLanes / 8; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    return s;
+}
+// Row i's value from a lane that has it.
+template <int kLanes>
+__device__ __forceinline__ float rope_of_row(float v, int i) {
+    return __shfl_sync(0xffffffffu, v, (i & 1 ? kLanes / 2 : 0) + (i & 2 ? kLanes / 4 : 0), kLanes);
+}
+
+// Where a team stands: its token, and its operand's heads.
+struct RopeAt {
+    bool live;
+    int b, t, which, h0, h1;
+};
+template <int kLanes>
+__device__ __forceinline__ RopeAt rope_at(const RopeParams& p, unsigned tok) {
+    RopeAt a;
+    a.live = tok < (unsigned)p.B * (unsigned)p.T;  // every lane stays for the exchanges
+    if (!a.live) tok = 0;
+    a.b = p.B == 1 ? 0 : (int)(tok / (unsigned)p.T);
+    a.t = (int)(tok - (unsigned)a.b * (unsigned)p.T);
+    int hb = blockIdx.y;
+    a.which = hb < p.blocks[0] ? 0 : hb < p.blocks[0] + p.blocks[1] ? 1 : 2;
+    hb -= a.which == 0 ? 0 : a.which == 1 ? p.blocks[0] : p.blocks[0] + p.blocks[1];
+    a.h0 = hb * p.heads_per_team;
+    a.h1 = min(a.h0 + p.heads_per_team, p.x[a.which].H);
+    return a;
+}
+// The angles of a team's token in the lane's four pairs (1, 0 where nothing turns); false, with
+// an error set, if its position is outside the tables.
+__device__ __forceinline__ bool rope_angles(const RopeParams& p, const RopeAt& a, const RopeLane& l, uint64_t (&c)[2],
+                                            uint64_t (&s)[2]) {
+    c[0] = c[1] = rope2(1.f, 1.f);
+    s[0] = s[1] = rope2(0.f, 0.f);
+    if (p.cos == nullptr || a.which == 2) return true;
+    const int pos = p.positions ? __ldg(p.positions + a.b * p.pos_sb + a.t) : a.t;
+    if ((unsigned)pos >= (unsigned)p.n_positions) {
+        if (a.live) atomicOr(p.err, kDevErrBadSeqlens);
+        return false;
+    }
+    if (l.angle >= 0) {
+        const long long at = (long long)pos * (p.rot >> 1) + l.angle;
+        const float4 x = __ldg(reinterpret_cast<const float4*>(p.cos + at)), y = __ldg(reinterpret_cast<const float4*>(p.sin + at));
+        c[0] = rope2(x.x, x.y), c[1] = rope2(x.z, x.w);
+        s[0] = rope2(y.x, y.y), s[1] = rope2(y.z, y.w);
+    }
+    return true;
 }
 
 // Forward and appending form. A team of D/8 lanes takes up to heads_per_team heads of one
-// operand of one token; kUnroll rows are loaded before the first is used.
+// operand of one token.
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) gqa_rope_fwd_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 4) gqa_rope_fwd_kernel(const __grid_constant__ RopeParams p) {
     constexpr int kLanes = D / 8;
-    constexpr int kUnroll = 4;
+    constexpr int kUnroll = kRopeUnroll;
     const int j = threadIdx.x % kLanes;
-    const long long team = (long long)blockIdx.x * (kRopeThreads / kLanes) + threadIdx.x / kLanes;
-    const int per_token = p.blocks[0] + p.blocks[1] + p.blocks[2];
-    long long tok = team / per_token;
-    int hb = (int)(team - tok * per_token);
-    const bool live = tok < (long long)p.B * p.T;  // every lane stays for the shuffles
-    if (!live) tok = hb = 0;
-    const int b = (int)(tok / p.T), t = (int)(tok - (long long)b * p.T);
-    int which = 0;
-    while (hb >= p.blocks[which]) hb -= p.blocks[which++];
-    const RopeRows& x = p.x[which];
+    const RopeAt a = rope_at<kLanes>(p, blockIdx.x * (kRopeThreads / kLanes) + threadIdx.x / kLanes);
+    const RopeRows& x = p.x[a.which];
     const RopeLane l = rope_lane<D, kInterleaved>(j, p.rot);
 
-    bool write = live;
-    long long out = (long long)b * x.out_sb + (long long)t * x.out_st;
-    if (p.slots != nullptr && which > 0) {
-        const int slot = p.slots[t];
+    bool write = a.live;
+    long long out = a.b * x.out_sb + a.t * x.out_st;
+    if (p.slots != nullptr && a.which > 0) {
+        const int slot = __ldg(p.slots + a.t);
         const int page = slot / p.page_size;
         if (slot < 0 || page >= p.num_pages) {
-            if (slot >= 0 && live && j == 0) atomicOr(p.err, kDevErrBadSeqlens);
+            if (slot >= 0 && a.live) atomicOr(p.err, kDevErrBadSeqlens);
             write = false;
             out = 0;
         } else {
-            out = (long long)page * x.out_sb + (long long)(slot - page * p.page_size) * x.out_st;
+            out = page * x.out_sb + (slot - page * p.page_size) * x.out_st;
         }
     }
-    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool turn = p.cos != nullptr && which < 2;
-    if (turn) {
-        const int pos = p.positions ? p.positions[(long long)b * p.pos_sb + t] : t;
-        if (pos < 0 || pos >= p.n_positions) {
-            if (live && j == 0) atomicOr(p.err, kDevErrBadSeqlens);
-            write = false;
-        } else if (l.angle >= 0) {
-            c = *reinterpret_cast<const float4*>(p.cos + (long long)pos * (p.rot >> 1) + l.angle);
-            s = *reinterpret_cast<const float4*>(p.sin + (long long)pos * (p.rot >> 1) + l.angle);
-        }
-    }
-    float w0[4], w1[4];
     const bool norm = x.weight != nullptr;
-    if (norm) {
-        rope_weight(x.weight, p.weight_fp32, l.e0, w0);
-        rope_weight(x.weight, p.weight_fp32, l.e1, w1);
+    // z_a = (r x_a)(w_a c) - (r x_b)(w_b s), z_b = (r x_b)(w_b c) + (r x_a)(w_a s)
+    uint64_t c[2], s[2];
+    if (!rope_angles(p, a, l, c, s)) write = false;
+    const RopePairs w = rope_weights<kInterleaved>(x.weight, p.weight_fp32, l);
+    uint64_t ac[2], as[2], bc[2], bs[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        ac[i] = rope2_mul(w.a[i], c[i]);
+        as[i] = rope2_mul(w.a[i], s[i]);
+        bc[i] = rope2_mul(w.b[i], c[i]);
+        bs[i] = rope2_neg(rope2_mul(w.b[i], s[i]));
     }
-    const int h0 = hb * p.heads_per_team, h1 = min(h0 + p.heads_per_team, x.H);
-    const __nv_bfloat16* in = x.in + (long long)b * x.in_sb + (long long)t * x.in_st;
-    for (int h = 0; h < p.heads_per_team; h += kUnroll) {
+    const bool copy = !norm && (p.cos == nullptr || a.which == 2 || l.angle < 0);  // these elements stay as they are
+    const __nv_bfloat16* in = x.in + a.b * x.in_sb + a.t * x.in_st;
+    for (int h = a.h0; h < a.h1; h += kUnroll) {
         uint2 u0[kUnroll], u1[kUnroll];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-            const int hh = h0 + h + i;
             u0[i] = u1[i] = make_uint2(0u, 0u);
-            if (live && h + i < p.heads_per_team && hh < h1) {
-                u0[i] = rope_load(in + hh * x.in_sh + l.e0);
-                u1[i] = rope_load(in + hh * x.in_sh + l.e1);
+            if (a.live && h + i < a.h1) {
+                u0[i] = rope_load(in + (h + i) * x.in_sh + l.e0);
+                u1[i] = rope_load(in + (h + i) * x.in_sh + l.e1);
             }
+        }
+        float r = 1.f;
+        if (norm) {
+            float sq[kUnroll];
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                const RopePairs f = rope_unpack<kInterleaved>(u0[i], u1[i]);
+                uint64_t v = rope2_mul(f.a[0], f.a[0]);
+                v = rope2_fma(f.a[1], f.a[1], v);
+                v = rope2_fma(f.b[0], f.b[0], v);
+                sq[i] = rope2_sum(rope2_fma(f.b[1], f.b[1], v));
+            }
+            r = rsqrtf(rope_sums<kLanes>(sq, j) * (1.f / D) + p.eps);
         }
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-            if (h + i >= p.heads_per_team) break;  // the same for every lane
-            const int hh = h0 + h + i;
-            float f0[4], f1[4];
-            rope_unpack(u0[i], f0);
-            rope_unpack(u1[i], f1);
-            float sq = 0.f;
+            if (!copy) {
+                RopePairs f = rope_unpack<kInterleaved>(u0[i], u1[i]);
+                RopePairs z;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sq += f0[e] * f0[e] + f1[e] * f1[e];
-            sq = rope_team_sum<kLanes>(sq);
-            if (norm) {
-                const float r = rsqrtf(sq * (1.f / D) + p.eps);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    f0[e] *= r * w0[e];
-                    f1[e] *= r * w1[e];
+                for (int e = 0; e < 2; ++e) {
+                    z.a[e] = rope2_fma(f.b[e], bs[e], rope2_mul(f.a[e], ac[e]));
+                    z.b[e] = rope2_fma(f.a[e], as[e], rope2_mul(f.b[e], bc[e]));
                 }
+                if (norm) {
+                    const float ri = rope_of_row<kLanes>(r, i);
+                    const uint64_t rr = rope2(ri, ri);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        z.a[e] = rope2_mul(z.a[e], rr);
+                        z.b[e] = rope2_mul(z.b[e], rr);
+                    }
+                }
+                rope_pack<kInterleaved>(z, u0[i], u1[i]);
             }
-            if (turn && l.angle >= 0) rope_turn<kInterleaved>(f0, f1, c, s, 1.f);
-            if (norm || turn) {
-                u0[i] = rope_pack(f0);
-                u1[i] = rope_pack(f1);
-            }
-            if (write && hh < h1) {
-                __nv_bfloat16* o = x.out + out + hh * x.out_sh;
+            if (write && h + i < a.h1) {
+                __nv_bfloat16* o = x.out + out + (h + i) * x.out_sh;
                 *reinterpret_cast<uint2*>(o + l.e0) = u0[i];
                 *reinterpret_cast<uint2*>(o + l.e1) = u1[i];
             }
@@ -231,140 +336,146 @@ __global__ void __launch_bounds__(kRopeThreads) gqa_rope_fwd_kernel(const RopePa
     }
 }
 
-// Backward. A CTA takes rows of one operand only, a strided share of its (token, head block)s,
-// and leaves one row of dw sums; gqa_rope_dw_kernel adds those up in a fixed order, so the
-// gradients do not change from run to run.
+// Backward. A CTA takes one head block (blockIdx.y) of a strided share of the tokens, and leaves one
+// row of dw sums; gqa_rope_dw_kernel adds those up in a fixed order, so the gradients do not
+// change from run to run.
+//   g = R^T dz,  dw += (g x) r,  dx = (r g) w - x (r^3 sum(g w x) / D)
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) gqa_rope_bwd_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) gqa_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
     constexpr int kLanes = D / 8;
     constexpr int kTeams = kRopeThreads / kLanes;
-    constexpr int kUnroll = 2;
+    constexpr int kUnroll = kRopeUnroll;
     __shared__ float sums[kTeams][D];
     const int j = threadIdx.x % kLanes, team = threadIdx.x / kLanes;
-    const int which = (int)blockIdx.x < p.q_blocks ? 0 : 1;
-    const RopeRows& x = p.x[which];
-    const int cta = which ? blockIdx.x - p.q_blocks : blockIdx.x;
-    const int ctas = which ? gridDim.x - p.q_blocks : p.q_blocks;
     const RopeLane l = rope_lane<D, kInterleaved>(j, p.rot);
-    const bool norm = x.weight != nullptr, turn = p.cos != nullptr;
-    float w0[4], w1[4], d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
-    if (norm) {
-        rope_weight(x.weight, p.weight_fp32, l.e0, w0);
-        rope_weight(x.weight, p.weight_fp32, l.e1, w1);
-    }
-    const long long units = (long long)p.B * p.T * p.blocks[which];
-    for (long long u0 = (long long)cta * kTeams; u0 < units; u0 += (long long)ctas * kTeams) {
-        long long u = u0 + team;
-        const bool live = u < units;
-        if (!live) u = 0;
-        const long long tok = u / p.blocks[which];
-        const int hb = (int)(u - tok * p.blocks[which]);
-        const int b = (int)(tok / p.T), t = (int)(tok - (long long)b * p.T);
-        bool use = live;
-        float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (turn) {
-            const int pos = p.positions ? p.positions[(long long)b * p.pos_sb + t] : t;
-            if (pos < 0 || pos >= p.n_positions) {
-                if (live && j == 0) atomicOr(p.err, kDevErrBadSeqlens);
-                use = false;
-            } else if (l.angle >= 0) {
-                c = *reinterpret_cast<const float4*>(p.cos + (long long)pos * (p.rot >> 1) + l.angle);
-                s = *reinterpret_cast<const float4*>(p.sin + (long long)pos * (p.rot >> 1) + l.angle);
-            }
-        }
-        const int h0 = hb * p.heads_per_team, h1 = min(h0 + p.heads_per_team, x.H);
-        const __nv_bfloat16* in = x.in + (long long)b * x.in_sb + (long long)t * x.in_st;
-        const __nv_bfloat16* gr = x.grad + (long long)b * x.grad_sb + (long long)t * x.grad_st;
-        __nv_bfloat16* out = x.out + (long long)b * x.out_sb + (long long)t * x.out_st;
-        for (int h = 0; h < p.heads_per_team; h += kUnroll) {
-            uint2 a0[kUnroll], a1[kUnroll], g0[kUnroll], g1[kUnroll];
+    const RopeAt first = rope_at<kLanes>(p, 0);
+    const RopeRows& x = p.x[first.which];
+    const bool norm = x.weight != nullptr;
+    const RopePairs w = rope_weights<kInterleaved>(x.weight, p.weight_fp32, l);
+    RopePairs dw;
+    dw.a[0] = dw.a[1] = dw.b[0] = dw.b[1] = rope2(0.f, 0.f);
+    const unsigned tokens = (unsigned)p.B * (unsigned)p.T;
+    for (unsigned base = blockIdx.x * kTeams; base < tokens; base += gridDim.x * kTeams) {  // the same for every lane
+        const RopeAt a = rope_at<kLanes>(p, base + team);
+        uint64_t c[2], s[2];
+        const bool use = rope_angles(p, a, l, c, s) && a.live;
+        const __nv_bfloat16* in = x.in + a.b * x.in_sb + a.t * x.in_st;
+        const __nv_bfloat16* gr = x.grad + a.b * x.grad_sb + a.t * x.grad_st;
+        __nv_bfloat16* out = x.out + a.b * x.out_sb + a.t * x.out_st;
+        const bool copy = !norm && l.angle < 0;
+        for (int h = a.h0; h < a.h1; h += kUnroll) {
+            uint2 x0[kUnroll], x1[kUnroll], g0[kUnroll], g1[kUnroll];
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
-                const int hh = h0 + h + i;
-                a0[i] = a1[i] = g0[i] = g1[i] = make_uint2(0u, 0u);
-                if (use && h + i < p.heads_per_team && hh < h1) {
-                    g0[i] = rope_load(gr + hh * x.grad_sh + l.e0);
-                    g1[i] = rope_load(gr + hh * x.grad_sh + l.e1);
+                x0[i] = x1[i] = g0[i] = g1[i] = make_uint2(0u, 0u);
+                if (use && h + i < a.h1) {
+                    g0[i] = rope_load(gr + (h + i) * x.grad_sh + l.e0);
+                    g1[i] = rope_load(gr + (h + i) * x.grad_sh + l.e1);
                     if (norm) {
-                        a0[i] = rope_load(in + hh * x.in_sh + l.e0);
-                        a1[i] = rope_load(in + hh * x.in_sh + l.e1);
+                        x0[i] = rope_load(in + (h + i) * x.in_sh + l.e0);
+                        x1[i] = rope_load(in + (h + i) * x.in_sh + l.e1);
                     }
                 }
             }
+            const auto back = [&](int i) {  // g of row i
+                const RopePairs d = rope_unpack<kInterleaved>(g0[i], g1[i]);
+                RopePairs g;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    g.a[e] = rope2_fma(d.b[e], s[e], rope2_mul(d.a[e], c[e]));
+                    g.b[e] = rope2_fma(d.a[e], rope2_neg(s[e]), rope2_mul(d.b[e], c[e]));
+                }
+                return g;
+            };
+            float r = 1.f, k = 0.f;  // of the lane's row of the four
+            if (norm) {
+                float sq[kUnroll], dot[kUnroll];
+#pragma unroll
+                for (int i = 0; i < kUnroll; ++i) {
+                    const RopePairs f = rope_unpack<kInterleaved>(x0[i], x1[i]), g = back(i);
+                    uint64_t u = rope2(0.f, 0.f), v = u;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        u = rope2_fma(f.a[e], f.a[e], u);
+                        u = rope2_fma(f.b[e], f.b[e], u);
+                        v = rope2_fma(rope2_mul(g.a[e], f.a[e]), w.a[e], v);
+                        v = rope2_fma(rope2_mul(g.b[e], f.b[e]), w.b[e], v);
+                    }
+                    sq[i] = rope2_sum(u);
+                    dot[i] = rope2_sum(v);
+                }
+                r = rsqrtf(rope_sums<kLanes>(sq, j) * (1.f / D) + p.eps);
+                k = -rope_sums<kLanes>(dot, j) * (1.f / D) * r * r * r;
+                // rows that are not there add nothing to dw, whatever eps is
+                if (!use || h + rope_row<kLanes>(j) >= a.h1) r = k = 0.f;
+            }
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
-                if (h + i >= p.heads_per_team) break;  // the same for every lane
-                const int hh = h0 + h + i;
-                const bool row = use && hh < h1;
-                float f0[4], f1[4], n0[4], n1[4];
-                rope_unpack(g0[i], f0);
-                rope_unpack(g1[i], f1);
-                if (turn && l.angle >= 0) rope_turn<kInterleaved>(f0, f1, c, s, -1.f);
-                if (norm) {
-                    rope_unpack(a0[i], n0);
-                    rope_unpack(a1[i], n1);
-                    float sq = 0.f, dot = 0.f;
+                uint2 u0 = g0[i], u1 = g1[i];
+                if (!copy) {
+                    RopePairs g = back(i);
+                    if (norm) {
+                        const RopePairs f = rope_unpack<kInterleaved>(x0[i], x1[i]);
+                        const float ri = rope_of_row<kLanes>(r, i), ki = rope_of_row<kLanes>(k, i);
+                        const uint64_t rr = rope2(ri, ri), kk = rope2(ki, ki);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        sq += n0[e] * n0[e] + n1[e] * n1[e];
-                        dot += f0[e] * w0[e] * n0[e] + f1[e] * w1[e] * n1[e];
+                        for (int e = 0; e < 2; ++e) {
+                            const uint64_t ga = rope2_mul(g.a[e], rr), gb = rope2_mul(g.b[e], rr);
+                            dw.a[e] = rope2_fma(ga, f.a[e], dw.a[e]);
+                            dw.b[e] = rope2_fma(gb, f.b[e], dw.b[e]);
+                            g.a[e] = rope2_fma(ga, w.a[e], rope2_mul(f.a[e], kk));
+                            g.b[e] = rope2_fma(gb, w.b[e], rope2_mul(f.b[e], kk));
+                        }
                     }
-                    sq = rope_team_sum<kLanes>(sq);
-                    dot = rope_team_sum<kLanes>(dot);
-                    // rows that are not there add nothing to dw, whatever eps is
-                    const float r = row ? rsqrtf(sq * (1.f / D) + p.eps) : 0.f;
-                    const float m = dot * r * (1.f / D);  // mean(e * n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        n0[e] *= r;
-                        n1[e] *= r;
-                        d0[e] += f0[e] * n0[e];
-                        d1[e] += f1[e] * n1[e];
-                        f0[e] = r * (f0[e] * w0[e] - n0[e] * m);
-                        f1[e] = r * (f1[e] * w1[e] - n1[e] * m);
-                    }
+                    rope_pack<kInterleaved>(g, u0, u1);
                 }
-                if (row) {
-                    *reinterpret_cast<uint2*>(out + hh * x.out_sh + l.e0) = rope_pack(f0);
-                    *reinterpret_cast<uint2*>(out + hh * x.out_sh + l.e1) = rope_pack(f1);
+                if (use && h + i < a.h1) {
+                    *reinterpret_cast<uint2*>(out + (h + i) * x.out_sh + l.e0) = u0;
+                    *reinterpret_cast<uint2*>(out + (h + i) * x.out_sh + l.e1) = u1;
                 }
             }
         }
     }
     if (!norm) return;  // uniform over the CTA
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        sums[team][l.e0 + e] = d0[e];
-        sums[team][l.e1 + e] = d1[e];
+    for (int e = 0; e < 2; ++e) {
+        float a0, a1, b0, b1;
+        f2_unpack(dw.a[e], a0, a1);
+        f2_unpack(dw.b[e], b0, b1);
+        if (kInterleaved) {
+            float* at = sums[team] + (e ? l.e1 : l.e0);
+            at[0] = a0, at[1] = b0, at[2] = a1, at[3] = b1;
+        } else {
+            sums[team][l.e0 + 2 * e] = a0, sums[team][l.e0 + 2 * e + 1] = a1;
+            sums[team][l.e1 + 2 * e] = b0, sums[team][l.e1 + 2 * e + 1] = b1;
+        }
     }
     __syncthreads();
     if (threadIdx.x < D) {
         float v = 0.f;
+#pragma unroll
         for (int i = 0; i < kTeams; ++i) v += sums[i][threadIdx.x];
-        p.partial[(long long)blockIdx.x * D + threadIdx.x] = v;
+        p.partial[((long long)blockIdx.y * gridDim.x + blockIdx.x) * D + threadIdx.x] = v;
     }
 }
 
-// dw[d] = sum of the CTAs' partial sums; CTA 0: queries, CTA 1: keys.
+// dw[d] = sum of the CTAs' partial sums; blockIdx.x 0: queries, 1: keys; 32 columns a CTA.
 template <int D>
-__global__ void __launch_bounds__(1024) gqa_rope_dw_kernel(const float* partial, int q_blocks, int blocks, float* dq_w,
-                                                           float* dk_w) {
-    constexpr int kGroups = 1024 / D;
-    __shared__ float sums[kGroups][D];
+__global__ void __launch_bounds__(1024) gqa_rope_dw_kernel(const float* partial, int q_rows, int rows, float* dq_w, float* dk_w) {
+    __shared__ float sums[32][33];
     float* out = blockIdx.x ? dk_w : dq_w;
     if (out == nullptr) return;
-    const int lo = blockIdx.x ? q_blocks : 0, hi = blockIdx.x ? blocks : q_blocks;
-    const int d = threadIdx.x % D, g = threadIdx.x / D;
+    const int lo = blockIdx.x ? q_rows : 0, hi = blockIdx.x ? rows : q_rows;
+    const int c = threadIdx.x & 31, g = threadIdx.x >> 5, d = blockIdx.y * 32 + c;
     float v = 0.f;
 #pragma unroll 8
-    for (int i = lo + g; i < hi; i += kGroups) v += partial[(long long)i * D + d];
-    sums[g][d] = v;
+    for (int i = lo + g; i < hi; i += 32) v += partial[(long long)i * D + d];
+    sums[g][c] = v;
     __syncthreads();
-    if (g == 0) {
-        v = 0.f;
-        for (int i = 0; i < kGroups; ++i) v += sums[i][d];
-        out[d] = v;
-    }
+    v = sums[c][g];  // column g, groups over the lanes
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+    if (c == 0) out[blockIdx.y * 32 + g] = v;
 }
 
 }  // namespace gqa

@@ -448,7 +448,8 @@ GQA_API gqa_status gqa_paged_plan(const int* seqlens, const int* keep, const int
  * over the D elements of each row. R turns each pair (a, b) of the first `rot` elements by the
  * angle of its position, (a c - b s, b c + a s); pairs are (i, i + rot/2), or (2i, 2i + 1) when
  * `interleaved`. Everything between the bf16 input and the bf16 output is fp32.
- *   q_weight, k_weight  [D] bf16, or fp32 when weight_fp32; NULL: that side is not normalised.
+ *   q_weight, k_weight  [D] bf16, or fp32 when weight_fp32, 16-byte aligned; NULL: that side is
+ *                  not normalised.
  *   cos, sin       fp32 [n_positions, rot/2], contiguous, 16-byte aligned; both NULL: no rotation.
  *   positions      int32: token t of batch b has position positions[b*positions_sb + t]; NULL: t.
  *   rot            a multiple of 8 in [8, D].
