@@ -282,16 +282,20 @@ __global__ void __launch_bounds__(kRopeThreads, 4) gqa_rope_fwd_kernel(const __g
         bs[i] = rope2_neg(rope2_mul(w.b[i], s[i]));
     }
     const bool copy = !norm && (p.cos == nullptr || a.which == 2 || l.angle < 0);  // these elements stay as they are
-    const __nv_bfloat16* in = x.in + a.b * x.in_sb + a.t * x.in_st;
+    // the lane's first group of the next head's row; its second is `gap` elements on
+    const __nv_bfloat16* in = x.in + a.b * x.in_sb + a.t * x.in_st + a.h0 * x.in_sh + l.e0;
+    __nv_bfloat16* dst = x.out + out + a.h0 * x.out_sh + l.e0;
+    const int gap = l.e1 - l.e0;
     for (int h = a.h0; h < a.h1; h += kUnroll) {
         uint2 u0[kUnroll], u1[kUnroll];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
             u0[i] = u1[i] = make_uint2(0u, 0u);
             if (a.live && h + i < a.h1) {
-                u0[i] = rope_load(in + (h + i) * x.in_sh + l.e0);
-                u1[i] = rope_load(in + (h + i) * x.in_sh + l.e1);
+                u0[i] = rope_load(in);
+                u1[i] = rope_load(in + gap);
             }
+            in += x.in_sh;
         }
         float r = 1.f;
         if (norm) {
@@ -328,10 +332,10 @@ __global__ void __launch_bounds__(kRopeThreads, 4) gqa_rope_fwd_kernel(const __g
                 rope_pack<kInterleaved>(z, u0[i], u1[i]);
             }
             if (write && h + i < a.h1) {
-                __nv_bfloat16* o = x.out + out + (h + i) * x.out_sh;
-                *reinterpret_cast<uint2*>(o + l.e0) = u0[i];
-                *reinterpret_cast<uint2*>(o + l.e1) = u1[i];
+                *reinterpret_cast<uint2*>(dst) = u0[i];
+                *reinterpret_cast<uint2*>(dst + gap) = u1[i];
             }
+            dst += x.out_sh;
         }
     }
 }
@@ -341,7 +345,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) gqa_rope_fwd_kernel(const __g
 // change from run to run.
 //   g = R^T dz,  dw += (g x) r,  dx = (r g) w - x (r^3 sum(g w x) / D)
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads, 3) gqa_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 2) gqa_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
     constexpr int kLanes = D / 8;
     constexpr int kTeams = kRopeThreads / kLanes;
     constexpr int kUnroll = kRopeUnroll;
@@ -359,40 +363,49 @@ __global__ void __launch_bounds__(kRopeThreads, 3) gqa_rope_bwd_kernel(const __g
         const RopeAt a = rope_at<kLanes>(p, base + team);
         uint64_t c[2], s[2];
         const bool use = rope_angles(p, a, l, c, s) && a.live;
-        const __nv_bfloat16* in = x.in + a.b * x.in_sb + a.t * x.in_st;
-        const __nv_bfloat16* gr = x.grad + a.b * x.grad_sb + a.t * x.grad_st;
-        __nv_bfloat16* out = x.out + a.b * x.out_sb + a.t * x.out_st;
+        const uint64_t ns[2] = {rope2_neg(s[0]), rope2_neg(s[1])};
+        const __nv_bfloat16* in = x.in + a.b * x.in_sb + a.t * x.in_st + a.h0 * x.in_sh + l.e0;
+        const __nv_bfloat16* gr = x.grad + a.b * x.grad_sb + a.t * x.grad_st + a.h0 * x.grad_sh + l.e0;
+        __nv_bfloat16* out = x.out + a.b * x.out_sb + a.t * x.out_st + a.h0 * x.out_sh + l.e0;
+        const int gap = l.e1 - l.e0;
         const bool copy = !norm && l.angle < 0;
         for (int h = a.h0; h < a.h1; h += kUnroll) {
             uint2 x0[kUnroll], x1[kUnroll], g0[kUnroll], g1[kUnroll];
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
                 x0[i] = x1[i] = g0[i] = g1[i] = make_uint2(0u, 0u);
-                if (use && h + i < a.h1) {
-                    g0[i] = rope_load(gr + (h + i) * x.grad_sh + l.e0);
-                    g1[i] = rope_load(gr + (h + i) * x.grad_sh + l.e1);
+                if (a.live && h + i < a.h1) {  // whether the position is good does not hold the loads up
+                    g0[i] = rope_load(gr);
+                    g1[i] = rope_load(gr + gap);
                     if (norm) {
-                        x0[i] = rope_load(in + (h + i) * x.in_sh + l.e0);
-                        x1[i] = rope_load(in + (h + i) * x.in_sh + l.e1);
+                        x0[i] = rope_load(in);
+                        x1[i] = rope_load(in + gap);
                     }
                 }
+                gr += x.grad_sh;
+                in += x.in_sh;
             }
-            const auto back = [&](int i) {  // g of row i
+            if (!use) {  // a bad position's rows may hold a NaN
+#pragma unroll
+                for (int i = 0; i < kUnroll; ++i) x0[i] = x1[i] = g0[i] = g1[i] = make_uint2(0u, 0u);
+            }
+            RopePairs gs[kUnroll];  // g
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
                 const RopePairs d = rope_unpack<kInterleaved>(g0[i], g1[i]);
-                RopePairs g;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    g.a[e] = rope2_fma(d.b[e], s[e], rope2_mul(d.a[e], c[e]));
-                    g.b[e] = rope2_fma(d.a[e], rope2_neg(s[e]), rope2_mul(d.b[e], c[e]));
+                    gs[i].a[e] = rope2_fma(d.b[e], s[e], rope2_mul(d.a[e], c[e]));
+                    gs[i].b[e] = rope2_fma(d.a[e], ns[e], rope2_mul(d.b[e], c[e]));
                 }
-                return g;
-            };
+            }
             float r = 1.f, k = 0.f;  // of the lane's row of the four
             if (norm) {
                 float sq[kUnroll], dot[kUnroll];
 #pragma unroll
                 for (int i = 0; i < kUnroll; ++i) {
-                    const RopePairs f = rope_unpack<kInterleaved>(x0[i], x1[i]), g = back(i);
+                    const RopePairs f = rope_unpack<kInterleaved>(x0[i], x1[i]);
+                    const RopePairs& g = gs[i];
                     uint64_t u = rope2(0.f, 0.f), v = u;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) gqa_rope_bwd_kernel(const __g
             for (int i = 0; i < kUnroll; ++i) {
                 uint2 u0 = g0[i], u1 = g1[i];
                 if (!copy) {
-                    RopePairs g = back(i);
+                    RopePairs& g = gs[i];
                     if (norm) {
                         const RopePairs f = rope_unpack<kInterleaved>(x0[i], x1[i]);
                         const float ri = rope_of_row<kLanes>(r, i), ki = rope_of_row<kLanes>(k, i);
@@ -430,9 +443,10 @@ __global__ void __launch_bounds__(kRopeThreads, 3) gqa_rope_bwd_kernel(const __g
                     rope_pack<kInterleaved>(g, u0, u1);
                 }
                 if (use && h + i < a.h1) {
-                    *reinterpret_cast<uint2*>(out + (h + i) * x.out_sh + l.e0) = u0;
-                    *reinterpret_cast<uint2*>(out + (h + i) * x.out_sh + l.e1) = u1;
+                    *reinterpret_cast<uint2*>(out) = u0;
+                    *reinterpret_cast<uint2*>(out + gap) = u1;
                 }
+                out += x.out_sh;
             }
         }
     }
