@@ -193,9 +193,11 @@ gqa_status kv4_rows(bool append, const void* k, const void* v, const void* k_poo
     p.num_pages = num_pages;
     if ((p.err = gqa::device_error_ptr()) == nullptr) return GQA_ERR_CUDA;
     const int per = gqa::kKv4Threads / (D / 8);
-    const long long ctas = (2LL * N * Hkv + per - 1) / per;
-    if (ctas > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)ctas);
+    // many rows: eight heads a team, to spread its set-up; few: the four it has in flight at a time
+    p.heads_per_team = 2LL * N * ((Hkv + 7) / 8) * (D / 8) >= (long long)sm_count() * 2048 ? 8 : gqa::kKv4Unroll;
+    p.blocks = (Hkv + p.heads_per_team - 1) / p.heads_per_team;
+    if (2LL * p.blocks > 65535) return GQA_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)((N + (long long)per - 1) / per), (unsigned)(2 * p.blocks));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (append) {
         if (D == 128)
