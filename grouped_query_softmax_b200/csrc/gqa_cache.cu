@@ -57,6 +57,32 @@ int sm_count() {
     return sms;
 }
 
+// ---------------------------------------------------------------- plan
+template <int kThreads, bool kCluster>
+gqa_status paged_plan(const gqa::PagedPlanParams& p, cudaStream_t stream) {
+    const auto kernel = gqa::gqa_paged_plan_kernel<kThreads, kCluster>;
+    const size_t smem = gqa::paged_plan_smem(p.S);
+    if (smem > 48 * 1024 - 1024 &&  // beside the kernel's static shared memory
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)gqa::paged_plan_smem(gqa::kPagedMaxSeqs)) != cudaSuccess)
+        return GQA_ERR_CUDA;
+    const long long work = std::max<long long>(((long long)p.max_tokens + 3) / 4, p.S);  // four tokens a thread
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    if (kCluster)
+        cfg.gridDim.x = attr.val.clusterDim.x = p.max_tokens > gqa::kPagedTokensAlone ? gqa::kPagedCluster : 1;
+    else
+        cfg.gridDim.x = (unsigned)std::min<long long>((work + kThreads - 1) / kThreads, sm_count());
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return launched(cudaLaunchKernelEx(&cfg, kernel, p));
+}
+
 // ---------------------------------------------------------------- norm and rotation
 gqa_status rope_params(gqa::RopeParams& p, const gqa_rope* r, int B, int T, int Hq, int Hkv, int D) {
     gqa_status st = check_heads(Hq, Hkv, D);
@@ -297,24 +323,10 @@ gqa_status gqa_paged_plan(const int* seqlens, const int* keep, const int* new_to
                            positions, slots,   free_count_out, S,       max_pages,  page_size,  num_pages,   free_capacity,
                            max_tokens, gqa::device_error_ptr()};
     if (p.err == nullptr) return GQA_ERR_CUDA;
-    const size_t smem = gqa::paged_plan_smem(S);
-    cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024 - 1024)  // beside the kernel's static shared memory
-        e = cudaFuncSetAttribute(gqa::gqa_paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)gqa::paged_plan_smem(gqa::kPagedMaxSeqs));
-    if (e != cudaSuccess) return GQA_ERR_CUDA;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = max_tokens > gqa::kPagedTokensAlone ? gqa::kPagedCluster : 1;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(attr.val.clusterDim.x);
-    cfg.blockDim = dim3(gqa::kPagedThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return launched(cudaLaunchKernelEx(&cfg, gqa::gqa_paged_plan_kernel, p));
+    const bool in_place = seqlens_out == seqlens || free_count_out == free_count;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (S <= gqa::kPagedFewSeqs) return in_place ? paged_plan<gqa::kPagedFewSeqs, true>(p, s) : paged_plan<gqa::kPagedFewSeqs, false>(p, s);
+    return in_place ? paged_plan<1024, true>(p, s) : paged_plan<1024, false>(p, s);
 }
 
 gqa_status gqa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int T, int Hq, int Hkv, int D,

@@ -7,15 +7,16 @@
 // pages are a stack: the released pages are pushed first, in the order of (request, page),
 // then the pages wanted are popped in the same order, so the result does not depend on timing.
 //
-// One launch. Every CTA of one cluster scans all lengths itself (S is small) and keeps the
-// running sums in shared memory; a cluster barrier separates the last read of the lengths from
-// the first write, so seqlens_out may be seqlens and free_count_out free_count. Nothing else
-// is read and written at once: pops read the list below free_count, pushes write it from
-// free_count on (a popped page that this call released is looked up in the table it came
-// from, not in the list), and a request that releases pages takes none. Calling again with the
-// same seqlens and free_count therefore gives the same result.
+// One launch. Every CTA scans all lengths itself (S is small) and keeps the running sums in shared
+// memory; the work after the scan is shared out. Nothing is read and written at once: pops read the
+// list below free_count, pushes write it from free_count on (a popped page that this call released
+// is looked up in the table it came from, not in the list), and a request that releases pages
+// takes none. Only where seqlens_out is seqlens, or free_count_out free_count, must every CTA have
+// read them before one writes: then the CTAs are one cluster with a barrier in between, else they
+// are as many as there is work for and need none. Calling again with the same seqlens and
+// free_count gives the same result.
 //
-// Bound by latency: a launch, three dependent global reads and two barriers.
+// Bound by latency: a launch, three dependent global reads and two block barriers.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -24,9 +25,9 @@
 
 namespace gqa {
 
-constexpr int kPagedThreads = 1024;
-constexpr int kPagedMaxSeqs = 8192;  // 5 ints a request of shared memory
-constexpr int kPagedCluster = 8;     // CTAs of the cluster when there are many tokens
+constexpr int kPagedMaxSeqs = 8192;      // 5 ints a request of shared memory
+constexpr int kPagedFewSeqs = 256;       // at most: blocks of that many threads, else of 1024
+constexpr int kPagedCluster = 8;         // CTAs of the cluster when there are many tokens
 constexpr int kPagedTokensAlone = 8192;  // tokens that one CTA writes alone
 
 struct PagedPlanParams {
@@ -59,36 +60,40 @@ __device__ __forceinline__ int paged_find(const int* first, int lo, int hi, int 
     return lo;
 }
 
-// Inclusive block scan of a 64-bit value; *total gets the block's sum. All threads call it.
-__device__ __forceinline__ unsigned long long paged_scan(unsigned long long v, unsigned long long* warp_sums,
-                                                         unsigned long long* total) {
+// Inclusive block scans of two 64-bit values; total gets the block's sums. All threads call it.
+template <int kThreads>
+__device__ __forceinline__ void paged_scan(unsigned long long (&v)[2], unsigned long long (*warp_sums)[32],
+                                           unsigned long long (&total)[2]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const unsigned long long o = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v += o;
-    }
-    if (lane == 31) warp_sums[warp] = v;
-    __syncthreads();
-    unsigned long long before = 0, all = 0;
-    const unsigned long long w = lane < kPagedThreads / 32 ? warp_sums[lane] : 0;
-    unsigned long long inc = w;
+    for (int d = 1; d < 32; d <<= 1)
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const unsigned long long o = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += o;
-    }
-    all = __shfl_sync(0xffffffffu, inc, 31);
-    before = __shfl_sync(0xffffffffu, inc - w, warp);
+        for (int i = 0; i < 2; ++i) {
+            const unsigned long long o = __shfl_up_sync(0xffffffffu, v[i], d);
+            if (lane >= d) v[i] += o;
+        }
+    if (lane == 31) warp_sums[0][warp] = v[0], warp_sums[1][warp] = v[1];
     __syncthreads();
-    *total = all;
-    return v + before;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const unsigned long long w = lane < kThreads / 32 ? warp_sums[i][lane] : 0;
+        unsigned long long inc = w;
+#pragma unroll
+        for (int d = 1; d < kThreads / 32; d <<= 1) {
+            const unsigned long long o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
+        }
+        total[i] = __shfl_sync(0xffffffffu, inc, kThreads / 32 - 1);
+        v[i] += __shfl_sync(0xffffffffu, inc - w, warp);
+    }
+    __syncthreads();
 }
 
-__global__ void __launch_bounds__(kPagedThreads, 1) gqa_paged_plan_kernel(const PagedPlanParams p) {
+template <int kThreads, bool kCluster>
+__global__ void __launch_bounds__(kThreads, 1) gqa_paged_plan_kernel(const __grid_constant__ PagedPlanParams p) {
     namespace cg = cooperative_groups;
     extern __shared__ int paged_smem[];
-    __shared__ unsigned long long warp_sums[kPagedThreads / 32];
+    __shared__ unsigned long long warp_sums[2][32];
     int* cu = paged_smem;             // [S + 1] first token of each request
     int* first_take = cu + p.S + 1;   // [S + 1] first popped page of each request
     int* first_give = first_take + p.S + 1;  // [S + 1] first pushed page of each request
@@ -99,7 +104,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) gqa_paged_plan_kernel(const 
     const int count = *p.free_count;
     bool bad = false;
     unsigned long long tokens = 0, pages = 0;  // running totals; pages: released << 32 | taken
-    for (int base = 0; base < p.S; base += kPagedThreads) {
+    for (int base = 0; base < p.S; base += kThreads) {
         const int s = base + threadIdx.x;
         int held = 0, keep = 0, added = 0;
         if (s < p.S) {
@@ -116,11 +121,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1) gqa_paged_plan_kernel(const 
         const int has = (int)(((long long)keep + added + p.page_size - 1) / p.page_size);
         const unsigned long long mine =
             has > had ? (unsigned long long)(has - had) : (unsigned long long)(had - has) << 32;
-        unsigned long long all;
-        const unsigned long long t = tokens + paged_scan((unsigned long long)added, warp_sums, &all) - added;
-        tokens += all;
-        const unsigned long long g = pages + paged_scan(mine, warp_sums, &all) - mine;
-        pages += all;
+        unsigned long long sums[2] = {(unsigned long long)added, mine}, all[2];
+        paged_scan<kThreads>(sums, warp_sums, all);
+        const unsigned long long t = tokens + sums[0] - added, g = pages + sums[1] - mine;
+        tokens += all[0];
+        pages += all[1];
         if (s < p.S) {
             cu[s] = (int)min(t, (unsigned long long)0x7fffffff);  // past it the call is refused below
             first_take[s] = (int)(g & 0xffffffffu);
@@ -140,11 +145,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) gqa_paged_plan_kernel(const 
         (long long)count + n_give < n_take || (long long)count + n_push > p.free_capacity)
         bad = true;
     bad = __syncthreads_or(bad);
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();  // every CTA has read the lengths and the count
+    if constexpr (kCluster) cg::this_cluster().sync();  // every CTA has read the lengths and the count
 
-    const int threads = (int)cluster.num_blocks() * kPagedThreads;
-    const int tid = (int)cluster.block_rank() * kPagedThreads + threadIdx.x;
+    const int threads = (int)gridDim.x * kThreads;
+    const int tid = (int)blockIdx.x * kThreads + threadIdx.x;
     if (bad) {  // nothing happens to the cache; the outputs describe an empty step
         if (tid == 0) {
             atomicOr(p.err, kDevErrBadSeqlens);
@@ -205,7 +209,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) gqa_paged_plan_kernel(const 
                 // pages taken by this call are computed again: another thread writes their entries
                 page = o < had_s[s] ? p.table[(size_t)s * p.max_pages + o] : taken(first_take[s] + (o - had_s[s]));
             }
-            if (page >= 0 && page < p.num_pages) slot[e] = page * p.page_size + (pos[e] - o * p.page_size);
+            if (page >= 0 && page < p.num_pages)
+                slot[e] = page * p.page_size + (pos[e] - o * p.page_size);
+            else
+                atomicOr(p.err, kDevErrBadSeqlens);
         }
         if (t0 + 4 <= p.max_tokens) {
             *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);

@@ -429,8 +429,8 @@ GQA_API gqa_status gqa_attn_bwd(const void* q, const void* k, const void* v, con
  *                  (keep[s] + t - cu[s]) and its cache row page * page_size + position %
  *                  page_size (the slots of the calls below). Tokens past the last request's
  *                  (padding of the step's batch) get position 0 and slot -1.
- *   page_size      16, 32, 64 or a multiple of 128; num_pages the pool's pages. A table entry
- *                  outside [0, num_pages) gives slot -1.
+ *   page_size      16, 32, 64 or a multiple of 128; num_pages the pool's pages. A token whose
+ *                  page number lies outside [0, num_pages) gets slot -1, and is reported.
  * Lengths live on the device and are checked there: if one lies outside its bounds, the tokens
  * exceed max_tokens, or the pages run out (or would overflow free_capacity), then cache and free
  * list stay as they are, the outputs describe an empty step (cu_seqlens 0, slots -1, seqlens_out
