@@ -14,6 +14,7 @@ library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -776,30 +777,37 @@ def _attn_fwd_varlen_paged(q, k_pool, v_pool, cu_seqlens_q, seqlens_q, seqlens_k
 
 
 # ---------------------------------------------------------------- around the attention calls
-def _on_device(**tensors):
-    """The CUDA device that all given tensors (None: left out) are on; it must be the current one."""
+@functools.lru_cache(maxsize=None)
+def _torch_once():
+    """torch, its dtypes and the current-stream query of the calls below, looked up once."""
     torch = _torch()
-    device = None
-    for name, t in tensors.items():
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the current stream without a Stream object
+    return torch, raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _on_device(names, *tensors):
+    """The index of the CUDA device that all given tensors (None: left out) are on; it must be the
+    current one."""
+    device = -2
+    for i, t in enumerate(tensors):
         if t is None:
             continue
-        if device is None:
-            device = t.device
-            if device.type != "cuda":
-                raise TypeError(f"{name} must be a CUDA tensor")
-        elif t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the first operand on {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the operands are on {device}, which is not the current device")
+        d = t.get_device()
+        if d != device:
+            if d < 0:
+                raise TypeError(f"{names.split()[i]} must be a CUDA tensor")
+            if device != -2:
+                raise ValueError(f"{names.split()[i]} is on cuda:{d}, the first operand on cuda:{device}")
+            device = d
+    if device != _torch_once()[0].cuda.current_device():
+        raise ValueError(f"the operands are on cuda:{device}, which is not the current device")
     return device
 
 
 def _keep_until(stream, *tensors):
     """Tensors allocated here for a call on another stream than the current one stay allocated
     until that stream has passed the call."""
-    if stream is None:
-        return
-    torch = _torch()
+    torch = _torch_once()[0]
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
     for t in tensors:
@@ -807,26 +815,40 @@ def _keep_until(stream, *tensors):
             t.record_stream(stream)
 
 
+def _stream_on(stream, device):
+    return _torch_once()[1](device) if stream is None else _stream_handle(stream)
+
+
 def _int32(t, name, shape=None):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_contiguous():
+    torch = _torch_once()[0]
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 tensor")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
     return t
 
 
+@functools.lru_cache(maxsize=4096)
+def _c_layout(sb, sh, st):
+    return GqaLayout(sb, sh, st)
+
+
+@functools.lru_cache(maxsize=4096)
+def _c_layout4(sb, sh):
+    return GqaKv4Layout(sb, sh)
+
+
 def _bf16_rows(t, name, shape=None, dims=4):
-    """Layout (sb, sh, st) of a bf16 operand [B, H, T, D], or [T, H, D] when dims is 3."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+    """Layout of a bf16 operand [B, H, T, D], or [T, H, D] when dims is 3."""
+    torch = _torch_once()[0]
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be a bf16 tensor")
     if t.dim() != dims or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must have the shape {tuple(shape) if shape else f'of {dims} axes'}, not {tuple(t.shape)}")
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name}: the last (D) axis must be contiguous")
-    return (st[0], st[1], st[2]) if dims == 4 else (0, st[1], st[0])
+    return _c_layout(st[0], st[1], st[2]) if dims == 4 else _c_layout(0, st[1], st[0])
 
 
 class PagedPlan(NamedTuple):
@@ -863,8 +885,8 @@ def paged_plan(seqlens, new_tokens, block_table, free_list, free_count, *, page_
         raise ValueError("block_table must be [S, max_pages] and free_list [capacity]")
     if _int32(free_count, "free_count").numel() != 1:
         raise ValueError("free_count must hold one value")
-    device = _on_device(seqlens=seqlens, new_tokens=new_tokens, block_table=block_table, free_list=free_list,
-                        free_count=free_count, keep=keep)
+    device = _on_device("seqlens new_tokens block_table free_list free_count keep", seqlens, new_tokens, block_table,
+                        free_list, free_count, keep)
     max_tokens = int(max_tokens)
     fresh = None
     if out is None:
@@ -872,54 +894,58 @@ def paged_plan(seqlens, new_tokens, block_table, free_list, free_count, *, page_
             raise ValueError("max_tokens must be positive")
         pad = -max_tokens % 4  # positions and slots start on 16 bytes
         fresh = seqlens.new_empty(2 * (max_tokens + pad) + 2 * S + 2)
-        pos, _, slots, _, cu, lens, count = fresh.split([max_tokens, pad, max_tokens, pad, S + 1, S, 1])
+        pos, _, slots, _, cu, lens, count = fresh.split_with_sizes((max_tokens, pad, max_tokens, pad, S + 1, S, 1))
         out = PagedPlan(lens, cu, pos, slots, count)
     else:
         for t, n, shape in zip(out, PagedPlan._fields, ((S,), (S + 1,), (max_tokens,), (max_tokens,), (1,))):
             _int32(t, n, shape)
-        _on_device(seqlens=seqlens, **out._asdict())
+        _on_device("seqlens " + " ".join(PagedPlan._fields), seqlens, *out)
     st = _lib.gqa_paged_plan(seqlens.data_ptr(), _ptr(keep), new_tokens.data_ptr(), block_table.data_ptr(),
                              free_list.data_ptr(), free_count.data_ptr(), out.seqlens_k.data_ptr(),
                              out.cu_seqlens.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
                              out.free_count.data_ptr(), S, block_table.shape[1], page_size, num_pages,
-                             free_list.numel(), max_tokens, _stream_handle(stream))
+                             free_list.numel(), max_tokens, _stream_on(stream, device))
     if st != GQA_OK:
         raise GqaError(st, "gqa_paged_plan")
-    _keep_until(stream, fresh)
+    if stream is not None:
+        _keep_until(stream, fresh)
     return out
 
 
 def _rope_args(D, B, T, q_weight, k_weight, eps, cos, sin, positions, interleaved):
-    """(GqaRope, operands by name)."""
-    torch = _torch()
-    r = GqaRope(eps=eps, interleaved=bool(interleaved))
-    kinds = set()
-    for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        if w.dtype not in (torch.bfloat16, torch.float32) or w.shape != (D,) or not w.is_contiguous():
-            raise TypeError(f"{n} must be a contiguous bf16 or fp32 tensor [{D}]")
-        kinds.add(w.dtype)
-        setattr(r, n, w.data_ptr())
-    if len(kinds) > 1:
-        raise TypeError("q_weight and k_weight must have the same type")
-    r.weight_fp32 = torch.float32 in kinds
+    """The GqaRope of a call."""
+    torch = _torch_once()[0]
+    weight = k_weight if q_weight is None else q_weight
+    if weight is not None:
+        for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is None:
+                continue
+            if w.dtype not in (torch.bfloat16, torch.float32) or w.shape != (D,) or not w.is_contiguous():
+                raise TypeError(f"{n} must be a contiguous bf16 or fp32 tensor [{D}]")
+            if w.dtype is not weight.dtype:
+                raise TypeError("q_weight and k_weight must have the same type")
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
+    pos_ptr = pos_sb = 0
     if cos is None:
         if positions is not None:
             raise ValueError("positions need cos and sin")
+        tables = (None, None, None, 0, 0, 0)
     else:
         for n, t in (("cos", cos), ("sin", sin)):
-            if t.dtype != torch.float32 or t.dim() != 2 or t.shape != cos.shape or not t.is_contiguous():
+            if t.dtype is not torch.float32 or t.dim() != 2 or t.shape != cos.shape or not t.is_contiguous():
                 raise TypeError(f"{n} must be a contiguous fp32 tensor [positions, rot / 2]")
-        r.cos, r.sin, r.n_positions, r.rot = cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1]
         if positions is not None:
             _int32(positions, "positions")
             if positions.shape != (T,) and positions.shape != (B, T):
                 raise ValueError(f"positions must be [{T}] or [{B}, {T}]")
-            r.positions, r.positions_sb = positions.data_ptr(), T if positions.dim() == 2 else 0
-    return r, {"q_weight": q_weight, "k_weight": k_weight, "cos": cos, "sin": sin, "positions": positions}
+            pos_ptr, pos_sb = positions.data_ptr(), T if positions.dim() == 2 else 0
+        tables = (cos.data_ptr(), sin.data_ptr(), pos_ptr, pos_sb, cos.shape[0], 2 * cos.shape[1])
+    return GqaRope(None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+                   *tables, bool(interleaved), weight is not None and weight.dtype is torch.float32, eps)
+
+
+_ROPE_NAMES = " q_weight k_weight cos sin positions"
 
 
 def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, eps=1e-6, cos=None, sin=None, positions=None,
@@ -939,19 +965,20 @@ def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, eps=1e-6, cos=None, sin=
     Hkv = k.shape[1]
     if k.shape != (B, Hkv, T, D):
         raise ValueError("q and k must be [B, Hq, T, D] and [B, Hkv, T, D]")
-    r, more = _rope_args(D, B, T, q_weight, k_weight, eps, cos, sin, positions, interleaved)
-    _on_device(q=q, k=k, q_out=q_out, k_out=k_out, **more)
+    r = _rope_args(D, B, T, q_weight, k_weight, eps, cos, sin, positions, interleaved)
+    device = _on_device("q k q_out k_out" + _ROPE_NAMES, q, k, q_out, k_out, q_weight, k_weight, cos, sin, positions)
     fresh_q = fresh_k = None
     if q_out is None:
         q_out = fresh_q = q.new_empty(q.shape)
     if k_out is None:
         k_out = fresh_k = k.new_empty(k.shape)
-    st = gqa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), B, T, Hq, Hkv, D, lq, lk,
-                          _bf16_rows(q_out, "q_out", q.shape), _bf16_rows(k_out, "k_out", k.shape), r,
-                          _stream_handle(stream))
+    st = _lib.gqa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), B, T, Hq, Hkv, D, lq, lk,
+                               _bf16_rows(q_out, "q_out", q.shape), _bf16_rows(k_out, "k_out", k.shape), r,
+                               _stream_on(stream, device))
     if st != GQA_OK:
         raise GqaError(st, "gqa_qk_norm_rope")
-    _keep_until(stream, fresh_q, fresh_k)
+    if stream is not None:
+        _keep_until(stream, fresh_q, fresh_k)
     return q_out, k_out
 
 
@@ -960,36 +987,48 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, *, q_weight=None, k_weight=None, eps=
     """Gradients (dq, dk, dq_weight, dk_weight) of ``qk_norm_rope(q, k, ...)`` for the gradients of
     its outputs (for instance ``attn_bwd``'s dq and dk). The weights' gradients are fp32 [D], None
     for a side without a weight. dq and dk may be dq_out and dk_out themselves."""
-    torch = _torch()
+    torch = _torch_once()[0]
     lq = _bf16_rows(q, "q")
     B, Hq, T, D = q.shape
     lk = _bf16_rows(k, "k")
     Hkv = k.shape[1]
     if k.shape != (B, Hkv, T, D):
         raise ValueError("q and k must be [B, Hq, T, D] and [B, Hkv, T, D]")
-    r, more = _rope_args(D, B, T, q_weight, k_weight, eps, cos, sin, positions, interleaved)
-    device = _on_device(dq_out=dq_out, dk_out=dk_out, q=q, k=k, dq=dq, dk=dk, workspace=workspace, **more)
+    r = _rope_args(D, B, T, q_weight, k_weight, eps, cos, sin, positions, interleaved)
+    device = _on_device("dq_out dk_out q k dq dk workspace" + _ROPE_NAMES, dq_out, dk_out, q, k, dq, dk, workspace, q_weight,
+                        k_weight, cos, sin, positions)
     fresh = []
     if dq is None:
         fresh.append(dq := q.new_empty(q.shape))
     if dk is None:
         fresh.append(dk := k.new_empty(k.shape))
-    dqw = torch.empty(D, dtype=torch.float32, device=device) if q_weight is not None else None
-    dkw = torch.empty(D, dtype=torch.float32, device=device) if k_weight is not None else None
-    fresh += [dqw, dkw]
-    if workspace is None and (dqw is not None or dkw is not None):
-        workspace = torch.empty(max(1, gqa_qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hkv, D)), dtype=torch.uint8,
-                                device=device)
-        fresh.append(workspace)
-    st = gqa_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
-                              dk.data_ptr(), _ptr(dqw), _ptr(dkw), B, T, Hq, Hkv, D,
-                              _bf16_rows(dq_out, "dq_out", q.shape), _bf16_rows(dk_out, "dk_out", k.shape), lq, lk,
-                              _bf16_rows(dq, "dq", q.shape), _bf16_rows(dk, "dk", k.shape), r, _ptr(workspace),
-                              workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                              _stream_handle(stream))
+    dqw = dkw = None
+    need = 0
+    if q_weight is not None or k_weight is not None:
+        if workspace is None:
+            need = gqa_qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hkv, D)
+        # one allocation: the weights' gradients behind the workspace
+        buf = torch.empty(need // 4 + 2 * D, dtype=torch.float32, device=q.device)
+        fresh.append(buf)
+        ws_ptr, ws_bytes = buf.data_ptr(), need
+        if workspace is not None:
+            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        _, dqw, dkw = buf.split_with_sizes((need // 4, D, D))
+        if q_weight is None:
+            dqw = None
+        if k_weight is None:
+            dkw = None
+    else:
+        ws_ptr, ws_bytes = None, 0
+    st = _lib.gqa_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
+                                   dk.data_ptr(), _ptr(dqw), _ptr(dkw), B, T, Hq, Hkv, D,
+                                   _bf16_rows(dq_out, "dq_out", q.shape), _bf16_rows(dk_out, "dk_out", k.shape), lq, lk,
+                                   _bf16_rows(dq, "dq", q.shape), _bf16_rows(dk, "dk", k.shape), r, ws_ptr, ws_bytes,
+                                   _stream_on(stream, device))
     if st != GQA_OK:
         raise GqaError(st, "gqa_qk_norm_rope_bwd")
-    _keep_until(stream, *fresh)
+    if stream is not None:
+        _keep_until(stream, *fresh)
     return dq, dk, dqw, dkw
 
 
@@ -1014,45 +1053,47 @@ def qk_norm_rope_append(q, k, v, k_pool, v_pool, slots, *, q_weight=None, k_weig
     sv = _bf16_rows(v_pool, "v_pool", k_pool.shape)
     if pool_layout == "NHD":
         pages, page, heads, _ = k_pool.shape
-        sk, sv = (sk[0], sk[2], sk[1]), (sv[0], sv[2], sv[1])
+        sk, sv = _c_layout(sk.sb, sk.st, sk.sh), _c_layout(sv.sb, sv.st, sv.sh)
     elif pool_layout == "HND":
         pages, heads, page, _ = k_pool.shape
     else:
         raise ValueError("pool_layout must be 'NHD' or 'HND'")
     if heads != Hkv or k_pool.shape[3] != D:
         raise ValueError("the pools' heads and rows must be k's")
-    r, more = _rope_args(D, 1, N, q_weight, k_weight, eps, cos, sin, positions, interleaved)
-    _on_device(q=q, k=k, v=v, k_pool=k_pool, v_pool=v_pool, slots=slots, q_out=q_out, **more)
+    r = _rope_args(D, 1, N, q_weight, k_weight, eps, cos, sin, positions, interleaved)
+    device = _on_device("q k v k_pool v_pool slots q_out" + _ROPE_NAMES, q, k, v, k_pool, v_pool, slots, q_out, q_weight,
+                        k_weight, cos, sin, positions)
     fresh = None
     if q_out is None:
         q_out = fresh = q.new_empty(q.shape)
-    st = gqa_qk_norm_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_pool.data_ptr(),
-                                 v_pool.data_ptr(), slots.data_ptr(), N, Hq, Hkv, D, page, pages, lq, lk, lv,
-                                 _bf16_rows(q_out, "q_out", q.shape, dims=3), sk, sv, r, _stream_handle(stream))
+    st = _lib.gqa_qk_norm_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_pool.data_ptr(),
+                                      v_pool.data_ptr(), slots.data_ptr(), N, Hq, Hkv, D, page, pages, lq, lk, lv,
+                                      _bf16_rows(q_out, "q_out", q.shape, dims=3), sk, sv, r, _stream_on(stream, device))
     if st != GQA_OK:
         raise GqaError(st, "gqa_qk_norm_rope_append")
-    _keep_until(stream, fresh)
+    if stream is not None:
+        _keep_until(stream, fresh)
     return q_out
 
 
 def kv4_pool(num_pages, num_heads, page_size, D, device=None):
     """A pool of zero rows for a paged cache held in 4 bits: uint8 [pages, Hkv, page, D / 2 + 4]."""
-    torch = _torch()
+    torch = _torch_once()[0]
     return torch.zeros((num_pages, num_heads, page_size, D // 2 + 4), dtype=torch.uint8,
                        device=torch.cuda.current_device() if device is None else device)
 
 
 def _kv4_layout(t, name, D, shape=None):
-    """Byte strides (page, head) of a 4-bit pool [pages, Hkv, page, D / 2 + 4]."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
+    """Layout of a 4-bit pool [pages, Hkv, page, D / 2 + 4]."""
+    torch = _torch_once()[0]
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8:
         raise TypeError(f"{name} must be a uint8 tensor")
     if t.dim() != 4 or t.shape[3] != D // 2 + 4 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must be [pages, Hkv, page, {D // 2 + 4}] (both pools alike), not {tuple(t.shape)}")
     st = t.stride()
     if st[3] != 1 or st[2] != t.shape[3]:
         raise ValueError(f"{name}: the rows of a page must be packed")
-    return st[0], st[1]
+    return _c_layout4(st[0], st[1])
 
 
 def kv4_append(k, v, k_pool, v_pool, slots, *, stream=None):
@@ -1066,9 +1107,9 @@ def kv4_append(k, v, k_pool, v_pool, slots, *, stream=None):
     sv = _kv4_layout(v_pool, "v_pool", D, k_pool.shape)
     if k_pool.shape[1] != Hkv:
         raise ValueError("the pools' heads must be k's")
-    _on_device(k=k, v=v, k_pool=k_pool, v_pool=v_pool, slots=slots)
-    st = gqa_kv4_append(k.data_ptr(), v.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), slots.data_ptr(), N, Hkv, D,
-                        k_pool.shape[2], k_pool.shape[0], lk, lv, sk, sv, _stream_handle(stream))
+    device = _on_device("k v k_pool v_pool slots", k, v, k_pool, v_pool, slots)
+    st = _lib.gqa_kv4_append(k.data_ptr(), v.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), slots.data_ptr(), N, Hkv, D,
+                             k_pool.shape[2], k_pool.shape[0], lk, lv, sk, sv, _stream_on(stream, device))
     if st != GQA_OK:
         raise GqaError(st, "gqa_kv4_append")
 
@@ -1076,7 +1117,7 @@ def kv4_append(k, v, k_pool, v_pool, slots, *, stream=None):
 def kv4_gather(k_pool, v_pool, slots, *, k=None, v=None, stream=None):
     """Rows ``slots`` (int32 [N]) of the 4-bit pools as bf16 (k, v) [N, Hkv, D]; a slot outside
     the pool gives zeros."""
-    torch = _torch()
+    torch = _torch_once()[0]
     if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
         raise TypeError("k_pool must be a uint8 tensor [pages, Hkv, page, D / 2 + 4]")
     pages, Hkv, page, row = k_pool.shape
@@ -1084,18 +1125,21 @@ def kv4_gather(k_pool, v_pool, slots, *, k=None, v=None, stream=None):
     sk = _kv4_layout(k_pool, "k_pool", D)
     sv = _kv4_layout(v_pool, "v_pool", D, k_pool.shape)
     N = _int32(slots, "slots").numel()
-    _on_device(k_pool=k_pool, v_pool=v_pool, slots=slots, k=k, v=v)
-    fresh_k = fresh_v = None
-    if k is None:
-        k = fresh_k = torch.empty((N, Hkv, D), dtype=torch.bfloat16, device=k_pool.device)
-    if v is None:
-        v = fresh_v = torch.empty((N, Hkv, D), dtype=torch.bfloat16, device=k_pool.device)
-    st = gqa_kv4_gather(k_pool.data_ptr(), v_pool.data_ptr(), k.data_ptr(), v.data_ptr(), slots.data_ptr(), N, Hkv, D,
-                        page, pages, sk, sv, _bf16_rows(k, "k", (N, Hkv, D), dims=3),
-                        _bf16_rows(v, "v", (N, Hkv, D), dims=3), _stream_handle(stream))
+    device = _on_device("k_pool v_pool slots k v", k_pool, v_pool, slots, k, v)
+    fresh = None
+    if k is None and v is None:
+        fresh = torch.empty((2, N, Hkv, D), dtype=torch.bfloat16, device=k_pool.device)
+        k, v = fresh.unbind(0)
+    elif k is None or v is None:
+        fresh = torch.empty((N, Hkv, D), dtype=torch.bfloat16, device=k_pool.device)
+        k, v = (fresh, v) if k is None else (k, fresh)
+    st = _lib.gqa_kv4_gather(k_pool.data_ptr(), v_pool.data_ptr(), k.data_ptr(), v.data_ptr(), slots.data_ptr(), N, Hkv, D,
+                             page, pages, sk, sv, _bf16_rows(k, "k", (N, Hkv, D), dims=3),
+                             _bf16_rows(v, "v", (N, Hkv, D), dims=3), _stream_on(stream, device))
     if st != GQA_OK:
         raise GqaError(st, "gqa_kv4_gather")
-    _keep_until(stream, fresh_k, fresh_v)
+    if stream is not None:
+        _keep_until(stream, fresh)
     return k, v
 
 
@@ -1108,7 +1152,7 @@ def attn_decode_kv4(q, k_pool, v_pool, seqlens_k, block_table, *, max_seqlen_k=N
     [B, max_pages]. ``workspace``: a uint8 CUDA tensor of gqa_attn_decode_kv4_workspace_bytes(...)
     bytes, allocated here when omitted.
     """
-    torch = _torch()
+    torch = _torch_once()[0]
     if not isinstance(q, torch.Tensor) or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.dim() not in (3, 4):
         raise TypeError("q must be a contiguous bf16 tensor [B, Hq, Tq, D] or [B, Hq, D]")
     B, Hq, D = q.shape[0], q.shape[1], q.shape[-1]
@@ -1122,23 +1166,24 @@ def attn_decode_kv4(q, k_pool, v_pool, seqlens_k, block_table, *, max_seqlen_k=N
         raise ValueError("block_table must be [B, max_pages]")
     max_pages = block_table.shape[1]
     max_seqlen_k = max_pages * page if max_seqlen_k is None else int(max_seqlen_k)
-    _on_device(q=q, k_pool=k_pool, v_pool=v_pool, seqlens_k=seqlens_k, block_table=block_table, out=out,
-               workspace=workspace)
+    device = _on_device("q k_pool v_pool seqlens_k block_table out workspace", q, k_pool, v_pool, seqlens_k, block_table, out,
+                        workspace)
     fresh_out = fresh_ws = None
     if out is None:
         out = fresh_out = q.new_empty(q.shape)
     elif out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 tensor shaped like q")
     if workspace is None:
-        need = gqa_attn_decode_kv4_workspace_bytes(B, Hq, Hkv, Tq, max_seqlen_k, D, window)
+        need = _lib.gqa_attn_decode_kv4_workspace_bytes(B, Hq, Hkv, Tq, max_seqlen_k, D, window)
         if need:
             workspace = fresh_ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    st = gqa_attn_decode_kv4(q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), out.data_ptr(), seqlens_k.data_ptr(),
-                             block_table.data_ptr(), page, pages, max_pages, B, Hq, Hkv, Tq, max_seqlen_k, D, sk, sv,
-                             float(scale or 0.0), window, _ptr(workspace),
-                             workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                             _stream_handle(stream))
+    st = _lib.gqa_attn_decode_kv4(q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), out.data_ptr(), seqlens_k.data_ptr(),
+                                  block_table.data_ptr(), page, pages, max_pages, B, Hq, Hkv, Tq, max_seqlen_k, D, sk, sv,
+                                  float(scale or 0.0), window, _ptr(workspace),
+                                  workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                  _stream_on(stream, device))
     if st != GQA_OK:
         raise GqaError(st, "gqa_attn_decode_kv4")
-    _keep_until(stream, fresh_out, fresh_ws)
+    if stream is not None:
+        _keep_until(stream, fresh_out, fresh_ws)
     return out

@@ -615,5 +615,5 @@ def test_two_streams_at_once_and_foreign_operands(gqa):
     for pair in outs:
         for o, wt in zip(pair, want):
             np.testing.assert_array_equal(bits_of(o), wt)
-    with pytest.raises(ValueError):
+    with pytest.raises(TypeError):
         gqa.attn_decode_kv4(qs[0], args[0], args[1], args[2], args[3].cpu())
