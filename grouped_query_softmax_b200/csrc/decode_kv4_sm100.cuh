@@ -26,6 +26,7 @@
 // in a fixed order. Bound by HBM: D + 8 bytes a key and KV head.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -34,7 +35,8 @@
 
 namespace gqa {
 
-constexpr int kD4MergeWarps = 4;
+constexpr int kD4MergeWarps = 8;
+constexpr int kD4MinRun = 2;  // tiles: shorter runs would leave more pieces to merge than they save
 
 struct Dec4Params {
     const __nv_bfloat16* q;  // [B, Hq, Tq, D]
@@ -70,7 +72,9 @@ struct Dec4Cfg {
     static constexpr int kCtasPerSm = NT == 4 ? 1 : 2;
     static constexpr int kQBytes = NT == 1 ? 0 : (D / 32) * NT * 32 * 16;  // Q fragments, in registers for one tile
     static constexpr int kWarpBytes = kStages * kStage + kQBytes;
-    static constexpr int kCtlOff = kWarps * kWarpBytes;
+    static constexpr int kMergeOff = kWarps * kWarpBytes;  // a CTA's state, for its cluster to read
+    static constexpr int kMergeBytes = (kRows * D + 2 * kRows) * 4;
+    static constexpr int kCtlOff = kMergeOff + kMergeBytes;
     struct Ctl {
         uint64_t full[kWarps][kStages];
         unsigned long long sums[kWarps];
@@ -81,6 +85,7 @@ struct Dec4Cfg {
     static constexpr int kBytes = kCtlOff + (int)sizeof(Ctl);
     static_assert(kTile % 16 == 0 && kWarpBytes % 16 == 0, "bulk copies need 16 bytes");
     static_assert(kCtasPerSm * (kBytes + 1024) <= 233472, "shared memory of an SM");
+    static_assert(kMergeBytes <= kWarpBytes, "a warp hands its state over in its ring");
 };
 
 // Tiles of one sequence: [first, first + n). A valid sequence has at least one, so that the
@@ -103,6 +108,7 @@ __device__ __forceinline__ Dec4Seq dec4_seq(const Dec4Params& p, int b) {
 // Start of run i when `total` tiles are cut into `runs`; total is below 2^52 (checked on the host)
 // and runs at most a few thousand.
 __device__ __forceinline__ unsigned long long dec4_cut(unsigned long long total, unsigned i, unsigned runs) {
+    if (total < 1u << 19 && runs <= 1u << 13) return (unsigned)total * i / runs;  // i <= runs: 32 bits do
     return total * i / runs;
 }
 
@@ -142,8 +148,12 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
     return d;
 }
 
-template <int D, int NT>
+// kCluster: the form for few tiles, where a second launch would cost more than it balances. A
+// cluster takes each unit, its warps equal parts of the unit's tiles, and the states are merged
+// through shared memory: in the CTA, then over the cluster.
+template <int D, int NT, bool kCluster>
 __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_decode_kv4_kernel(const Dec4Params p) {
+    namespace cg = cooperative_groups;
     using C = Dec4Cfg<D, NT>;
     constexpr int kStages = C::kStages;
     constexpr int kWarps = C::kWarps;
@@ -171,53 +181,73 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
     const int units = p.Hkv * p.n_rc;  // units of a sequence
     const auto work_of = [&](int b) { return b < p.B ? (unsigned long long)dec4_seq<kKeys>(p, b).n * units : 0ull; };
     const unsigned run = warp * gridDim.x + blockIdx.x;
-    const bool one_pass = p.B <= C::kThreads;
-    unsigned long long total = 0;
-    if (!one_pass) {
-        for (int b = threadIdx.x; b < p.B; b += C::kThreads) total += work_of(b);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-        if (lane == 0) ctl->sums[warp] = total;
-        __syncthreads();
-        total = 0;
-        for (int w = 0; w < kWarps; ++w) total += ctl->sums[w];
-        __syncthreads();
-    }
-    unsigned runs = 0;
-    unsigned long long before = 0;  // tiles of the rounds of sequences already seen
-    for (int b0 = 0; b0 < p.B; b0 += C::kThreads) {
-        const int b = b0 + threadIdx.x;
-        const unsigned long long x = work_of(b);
-        unsigned long long inc = x;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, d);
-            if (lane >= d) inc += y;
+    unsigned long long at, end;  // this warp's tiles
+    unsigned long long seq0;     // tiles before sequence b
+    int b;
+    Dec4Seq s;
+    if constexpr (kCluster) {
+        const unsigned ctas = cg::this_cluster().num_blocks(), unit = blockIdx.x / ctas;
+        b = (int)(unit / (unsigned)units);
+        s = dec4_seq<kKeys>(p, b);
+        if (s.n == 0) {  // the whole cluster leaves
+            if (threadIdx.x == 0) atomicOr(p.err, kDevErrBadSeqlens);
+            return;
         }
-        if (lane == 31) ctl->sums[warp] = inc;
-        __syncthreads();
-        unsigned long long lo = before + inc - x;
-        for (int w = 0; w < warp; ++w) lo += ctl->sums[w];
-        for (int w = 0; w < kWarps; ++w) before += ctl->sums[w];
-        if (one_pass) total = before;
-        runs = (unsigned)min((unsigned long long)gridDim.x * kWarps, total);
-        for (int w = 0; w < kWarps; ++w) {
-            const unsigned r = w * gridDim.x + blockIdx.x;
-            const unsigned long long first = r < runs ? dec4_cut(total, r, runs) : total;
-            if (lo <= first && first < lo + x) {
-                ctl->b[w] = b;
-                ctl->first[w] = lo;
+        const unsigned i = cg::this_cluster().block_rank() * kWarps + warp;
+        seq0 = 0;
+        at = (unsigned long long)(unit - b * units) * s.n;
+        end = at + dec4_cut(s.n, i + 1, ctas * kWarps);
+        at += dec4_cut(s.n, i, ctas * kWarps);
+        __syncthreads();  // the barriers and the flag are set up
+    } else {
+        const bool one_pass = p.B <= C::kThreads;
+        unsigned long long total = 0;
+        if (!one_pass) {
+            for (int b = threadIdx.x; b < p.B; b += C::kThreads) total += work_of(b);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+            if (lane == 0) ctl->sums[warp] = total;
+            __syncthreads();
+            total = 0;
+            for (int w = 0; w < kWarps; ++w) total += ctl->sums[w];
+            __syncthreads();
+        }
+        unsigned runs = 0;
+        unsigned long long before = 0;  // tiles of the rounds of sequences already seen
+        for (int b0 = 0; b0 < p.B; b0 += C::kThreads) {
+            const int b = b0 + threadIdx.x;
+            const unsigned long long x = work_of(b);
+            unsigned long long inc = x;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += y;
             }
+            if (lane == 31) ctl->sums[warp] = inc;
+            __syncthreads();
+            unsigned long long lo = before + inc - x;
+            for (int w = 0; w < warp; ++w) lo += ctl->sums[w];
+            for (int w = 0; w < kWarps; ++w) before += ctl->sums[w];
+            if (one_pass) total = before;
+            runs = (unsigned)min((unsigned long long)gridDim.x * kWarps, (total + kD4MinRun - 1) / kD4MinRun);
+            for (int w = 0; w < kWarps; ++w) {
+                const unsigned r = w * gridDim.x + blockIdx.x;
+                const unsigned long long first = r < runs ? dec4_cut(total, r, runs) : total;
+                if (lo <= first && first < lo + x) {
+                    ctl->b[w] = b;
+                    ctl->first[w] = lo;
+                }
+            }
+            if (blockIdx.x == 0 && b < p.B && x == 0) atomicOr(p.err, kDevErrBadSeqlens);
+            __syncthreads();
         }
-        if (blockIdx.x == 0 && b < p.B && x == 0) atomicOr(p.err, kDevErrBadSeqlens);
-        __syncthreads();
+        if (run >= runs) return;
+        at = dec4_cut(total, run, runs);
+        end = dec4_cut(total, run + 1, runs);
+        b = ctl->b[warp];
+        seq0 = ctl->first[warp];
+        s = dec4_seq<kKeys>(p, b);
     }
-    if (run >= runs) return;
-    unsigned long long at = dec4_cut(total, run, runs);
-    const unsigned long long end = dec4_cut(total, run + 1, runs);
-    int b = ctl->b[warp];
-    unsigned long long seq0 = ctl->first[warp];
-    Dec4Seq s = dec4_seq<kKeys>(p, b);
 
     const int box = min(p.page_size, kKeys);  // rows of one bulk copy
     const int boxes = kKeys / box;
@@ -227,14 +257,14 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
     int stage = 0;
     uint32_t phase = 0;
 
-    while (at < end) {
-        while (at >= seq0 + (unsigned long long)s.n * units) {  // sequences without work have n = 0
+    do {  // a warp of a cluster without a tile still joins the merge
+        while (!kCluster && at >= seq0 + (unsigned long long)s.n * units) {  // sequences without work have n = 0
             seq0 += (unsigned long long)s.n * units;
             s = dec4_seq<kKeys>(p, ++b);
         }
         // ---- the piece: tiles [t0, t1) of unit u of sequence b
         const unsigned long long in_seq = at - seq0;
-        const int u = (int)(in_seq / (unsigned)s.n);
+        const int u = kCluster ? (int)(blockIdx.x / cg::this_cluster().num_blocks()) - b * units : (int)(in_seq / (unsigned)s.n);
         const int t0 = (int)(in_seq - (unsigned long long)u * s.n);
         const int t1 = (int)min((unsigned long long)s.n, t0 + (end - at));
         at += t1 - t0;
@@ -377,7 +407,8 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                         phase ^= 1u;
                     }
                 }
-                return;  // no other warp waits for this one
+                if constexpr (kCluster) break;  // the others wait in the merge
+                return;                         // no other warp waits for this one
             }
             const uint32_t* K = reinterpret_cast<const uint32_t*>(ring + stage * C::kStage);
             const uint32_t* V = K + C::kTile / 4;
@@ -575,6 +606,66 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
         }
         if constexpr (NT > 1) __syncwarp();  // every lane has read the Q fragments
 
+        if constexpr (kCluster) {
+            // ---- merge: the warp's state through its ring, the CTA's through its own place
+            const float down = dec4_pow2(dec4_exponent(top_step) + 10);  // 2^24 / up_step
+            const auto state = [&](uint8_t* base) { return reinterpret_cast<float*>(base); };  // m, l of each row, then O
+            float* mine = state(ring);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) {
+                        l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], d);
+                        beta[nt][x] += __shfl_xor_sync(0xffffffffu, beta[nt][x], d);
+                    }
+                    const int n = 8 * nt + 2 * t + x;
+                    if (g == 0) mine[n] = m[nt][x], mine[C::kRows + n] = l[nt][x];
+#pragma unroll
+                    for (int i = 0; i < kMT; ++i)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float o = oacc[i][nt][2 * r + x] * (i % 2 ? 0.0625f : 1.f);  // odd codes count 16 times
+                            mine[2 * C::kRows + n * D + 64 * (i / 4) + 32 * r + 4 * g + i % 4] =
+                                fmaf(o - eights[nt][x], down, beta[nt][x]);
+                        }
+                }
+            __syncthreads();
+            cg::cluster_group cluster = cg::this_cluster();
+            float* ours = state(dec4_smem + C::kMergeOff);
+            // element (row, d) of the sum of `n` states at `at(i)`
+            const auto merged = [&](int n, auto at, int row, int d, float& top, float& sum) {
+                top = -INFINITY;
+                for (int i = 0; i < n; ++i) top = fmaxf(top, at(i)[row]);
+                const float mu = top == -INFINITY ? 0.f : top;
+                float acc = 0.f;
+                sum = 0.f;
+#pragma unroll 8
+                for (int i = 0; i < n; ++i) {
+                    const float f = ex2_approx(at(i)[row] - mu);
+                    sum += at(i)[C::kRows + row] * f;
+                    acc += at(i)[2 * C::kRows + row * D + d] * f;
+                }
+                return acc;
+            };
+            for (int idx = threadIdx.x; idx < nrows * D; idx += C::kThreads) {
+                const int row = idx / D, d = idx % D;
+                float top, sum;
+                const float acc = merged(kWarps, [&](int i) { return state(dec4_smem + i * C::kWarpBytes); }, row, d, top, sum);
+                ours[2 * C::kRows + idx] = acc;
+                if (d == 0) ours[row] = top, ours[C::kRows + row] = sum;
+            }
+            cluster.sync();
+            for (int idx = cluster.block_rank() * C::kThreads + threadIdx.x; idx < nrows * D; idx += cluster.num_blocks() * C::kThreads) {
+                const int row = idx / D, d = idx % D;
+                float top, sum;
+                const float acc = merged(cluster.num_blocks(), [&](int i) { return cluster.map_shared_rank(ours, i); }, row, d, top, sum);
+                p.o[(row0 + row) * D + d] = __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum);  // a row that sees no key: 0
+            }
+            cluster.sync();  // the states are read
+            return;
+        }
         // ---- the piece's rows: final if it is a whole unit, else partial. A row that sees no key of
         // the piece: 0, and weight 0 in the merge (NaN stays NaN).
         const bool whole = t0 == 0 && t1 == s.n;
@@ -616,7 +707,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                             *reinterpret_cast<float4*>(p.part + (part + n) * D + d) = make_float4(v[0], v[1], v[2], v[3]);
                     }
             }
-    }
+    } while (at < end);
 }
 
 // Merge the pieces of the units that were cut between warps, in run order: one block a row, of
@@ -644,7 +735,7 @@ __global__ void __launch_bounds__(32 * kD4MergeWarps) gqa_decode_kv4_merge_kerne
     for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
     if (M == -INFINITY) M = 0.f;
     float sum = 0.f, acc[E] = {};
-#pragma unroll 4
+#pragma unroll 8
     for (int c = c0 + warp; c <= c1; c += kD4MergeWarps) {
         const float f = ex2_approx(p.part_lse[at(c)] - M);
         const float* src = p.part + at(c) * D + lane * E;

@@ -259,8 +259,11 @@ int dec4_nt(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 struct Dec4Plan {
     int nt, n_rc, ctas, warps;  // warps: of a CTA
+    int cluster;                // CTAs of a unit's cluster, 0: runs of tiles and a merge
     size_t part, lse, ends, bytes;  // the workspace's parts and size
 };
+constexpr int kDec4MergeRounds = 4;  // rounds of tiles that take as long as the merge's launch
+constexpr int kDec4MostRounds = 8;   // of a cluster: lengths may differ, and only even runs balance that
 template <int D, int NT>
 Dec4Plan dec4_plan_for(int B, int Hkv, int rows, int Tq, int max_seqlen_k, int window) {
     using C = gqa::Dec4Cfg<D, NT>;
@@ -272,11 +275,21 @@ Dec4Plan dec4_plan_for(int B, int Hkv, int rows, int Tq, int max_seqlen_k, int w
     const long long keys = window > 0 ? std::min<long long>(max_seqlen_k, (long long)window + Tq + C::kKeys) : max_seqlen_k;
     const long long tiles = (long long)B * Hkv * r.n_rc * ((keys + C::kKeys - 1) / C::kKeys);
     r.ctas = (int)std::min<long long>((long long)sm_count() * C::kCtasPerSm, tiles);
-    const size_t slots = tiles > 1 ? (size_t)2 * r.ctas * r.warps * C::kRows : 0;
+    // A cluster a unit, if they all run at once (16 CTAs have to fit a GPC together: half the places)
+    // and have little more to do than the even runs, which pay for their merge with a second launch.
+    const long long units = (long long)B * Hkv * r.n_rc, of_unit = tiles / units;
+    const long long places = (long long)sm_count() * C::kCtasPerSm;
+    int cluster = 1;
+    while (cluster < 16 && cluster * C::kWarps < of_unit && units * 2 * cluster <= (cluster < 8 ? places : places / 2)) cluster *= 2;
+    const long long rounds = (of_unit + cluster * C::kWarps - 1) / (cluster * C::kWarps);
+    const long long even = (tiles + (long long)r.ctas * r.warps - 1) / ((long long)r.ctas * r.warps);
+    r.cluster = units * cluster <= places && rounds <= kDec4MostRounds && rounds <= even + kDec4MergeRounds ? cluster : 0;
+    if (r.cluster) r.ctas = (int)(units * cluster);
+    const size_t slots = !r.cluster ? (size_t)2 * r.ctas * r.warps * C::kRows : 0;
     r.part = 0;
     r.lse = gqa::round256(slots * D * sizeof(float));
     r.ends = r.lse + gqa::round256(slots * sizeof(float));
-    r.bytes = tiles > 1 ? r.ends + (size_t)B * Hkv * r.n_rc * sizeof(int2) : 0;
+    r.bytes = !r.cluster ? r.ends + (size_t)B * Hkv * r.n_rc * sizeof(int2) : 0;
     return r;
 }
 Dec4Plan dec4_plan(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, int window) {
@@ -293,11 +306,22 @@ Dec4Plan dec4_plan(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, int 
 template <int D, int NT>
 gqa_status launch_dec4(const gqa::Dec4Params& p, const Dec4Plan& r, cudaStream_t stream) {
     using C = gqa::Dec4Cfg<D, NT>;
-    cudaError_t e = cudaFuncSetAttribute(gqa::gqa_decode_kv4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         C::kBytes);
+    const auto kernel = r.cluster ? gqa::gqa_decode_kv4_kernel<D, NT, true> : gqa::gqa_decode_kv4_kernel<D, NT, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+    if (e == cudaSuccess && r.cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return GQA_ERR_CUDA;
-    gqa::gqa_decode_kv4_kernel<D, NT><<<(unsigned)r.ctas, C::kThreads, C::kBytes, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess || r.bytes == 0) return launched(e);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = r.cluster ? r.cluster : 1;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)r.ctas);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kBytes;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess || r.cluster) return launched(e);
     const dim3 grid((unsigned)p.B, (unsigned)(p.Hq * p.Tq));
     gqa::gqa_decode_kv4_merge_kernel<D, NT><<<grid, 32 * gqa::kD4MergeWarps, 0, stream>>>(p);
     return launched(cudaGetLastError());

@@ -121,6 +121,11 @@ def test_kv4_rows_reject_bad_arguments(gqa, gather, kw, status):
     assert kv4(gqa, gather, **kw) == status
 
 
+# enough work for runs of tiles that cut units, whose partial states need a workspace
+MANY = dict(B=64, Hq=32, Hkv=8, max_seqlen_k=32768, max_pages=512, k_layout=(8 * 64 * 68, 64 * 68),
+            v_layout=(8 * 64 * 68, 64 * 68))
+
+
 def dec(gqa, **kw):
     pool = (2 * 64 * 68, 64 * 68)
     a = dict(q=P, k_pool=P, v_pool=P, o=P, seqlens_k=P, block_table=P, page_size=64, num_pages=100, max_pages=16, B=2,
@@ -136,7 +141,7 @@ def dec(gqa, **kw):
     (dict(page_size=48), 1), (dict(num_pages=0), 1), (dict(max_pages=0), 1), (dict(max_seqlen_k=0), 1),
     (dict(max_seqlen_k=(1 << 30) + 1), 2), (dict(softmax_scale=float("nan")), 1), (dict(softmax_scale=float("inf")), 1),
     (dict(v_layout=(2 * 64 * 68, 64 * 68 - 16)), 1), (dict(k_layout=(2 * 64 * 68 + 4, 64 * 68)), 1),
-    (dict(workspace=None), 3), (dict(workspace=P + 64), 3), (dict(workspace_bytes=100), 3),
+    (dict(MANY, workspace=None), 3), (dict(MANY, workspace=P + 64), 3), (dict(MANY, workspace_bytes=100), 3),
     (dict(B=1 << 20, Hq=1 << 10, Hkv=1 << 10, Tq=16), 2),
 ])
 def test_decode_rejects_bad_arguments(gqa, kw, status):
@@ -144,11 +149,10 @@ def test_decode_rejects_bad_arguments(gqa, kw, status):
 
 
 def test_workspace_sizes(gqa):
-    assert gqa.gqa_attn_decode_kv4_workspace_bytes(1, 4, 1, 1, 32, 128) == 0  # a single tile is never cut
-    n = gqa.gqa_attn_decode_kv4_workspace_bytes(1, 8, 8, 1, 1024, 128)
-    assert n > 0  # partial states of the units that are cut
-    assert n < gqa.gqa_attn_decode_kv4_workspace_bytes(1, 8, 8, 1, 32768, 128) <= 64 << 20
-    assert gqa.gqa_attn_decode_kv4_workspace_bytes(1, 8, 8, 17, 1024, 128) == 0
+    size = gqa.gqa_attn_decode_kv4_workspace_bytes
+    assert size(1, 4, 1, 1, 32, 128) == 0 and size(1, 32, 8, 1, 4099, 128) == 0  # merged through shared memory
+    assert 0 < size(64, 32, 8, 1, 32768, 128) <= 64 << 20
+    assert size(64, 32, 8, 17, 32768, 128) == 0
     assert gqa.gqa_qk_norm_rope_bwd_workspace_bytes(1, 16, 8, 2, 128) % 256 == 0
     assert gqa.gqa_qk_norm_rope_bwd_workspace_bytes(1, 16, 8, 3, 128) == 0
 
