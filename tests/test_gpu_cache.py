@@ -261,6 +261,7 @@ def test_norm_rope_gradient_matches_differences_of_the_kernel(gqa):
 def test_norm_rope_bad_positions_leave_their_rows(gqa):
     torch = torch_mod()
     q, k = to_dev(gi.normal_bf16(28, 0, (1, 4, 6, 64))), to_dev(gi.normal_bf16(29, 1, (1, 2, 6, 64)))
+    q[:, :, 4], k[:, :, 1] = float("nan"), float("inf")   # rows at bad positions: no part in any gradient
     cos, sin = ref.angles(10, 64)
     how = dict(cos=_dev(cos), sin=_dev(sin), q_weight=torch.ones(64, device="cuda"), k_weight=torch.ones(64, device="cuda"))
     good = gqa.qk_norm_rope(q, k, positions=_i32([0, 1, 2, 3, 4, 5]), **how)
@@ -387,6 +388,12 @@ DECODE = [
     (12, 2, 3, [40, 999, 16], 64, 100, 32), (32, 1, 1, [130, 1, 2500], 128, 0, 64), (6, 2, 16, [16, 17, 300], 128, 0, 256),
     (8, 1, 16, [15, 640], 64, 33, 128), (32, 8, 1, [5000, 64, 3333, 1], 128, 1000, 64), (8, 8, 2, [700, 4, 2048], 128, 1, 16),
     (4, 1, 16, [1000, 33], 128, 0, 384), (8, 2, 1, [100] * 300, 64, 0, 16),
+    # more units than clusters fit at once: runs of tiles that cut units, and the merge; a long
+    # sequence in many pieces among short ones
+    (32, 8, 1, [(37 * i) % 700 for i in range(44)], 128, 0, 32), (32, 2, 1, [(91 * i) % 300 for i in range(160)], 128, 0, 64),
+    (32, 1, 1, [(53 * i) % 200 for i in range(155)], 128, 90, 16), (8, 1, 4, [(29 * i) % 150 for i in range(160)], 64, 0, 128),
+    (16, 2, 2, [7000] + [i % 60 for i in range(170)], 64, 0, 64), (4, 4, 1, [0] * 60 + [9000] + [0, 3] * 30, 128, 0, 16),
+    (8, 1, 1, [1, 2500] * 160, 64, 2000, 32),
 ]
 
 
@@ -446,20 +453,23 @@ def test_decode_kv4_strided_pools_scale_and_bad_pages(gqa):
     _near(from_dev(o), want[:, :, 0], 2 * tol[:, :, 0], "strided")   # scale 0.3: scores' error grows by 3.4 x 2^-14
 
 
-def test_decode_kv4_lengths_outside_their_range(gqa):
+@pytest.mark.parametrize("extra", [0, 230])
+def test_decode_kv4_lengths_outside_their_range(gqa, extra):
+    """Beside valid sequences, few (a cluster each) and many (runs of tiles)."""
     torch = torch_mod()
-    lens, Hq, Hkv, D, page = [200, 90, 64], 8, 2, 64, 16
+    lens, Hq, Hkv, D, page = [200, 90, 64] + [33] * extra, 8, 2, 64, 16
     kp, vp, table = _kv4_pools(lens, Hkv, D, page, 55)
-    q = gi.normal_bf16(56, gi.TENSOR_Q, (3, Hq, 1, D))
+    q = gi.normal_bf16(56, gi.TENSOR_Q, (len(lens), Hq, 1, D))
     want, tol = ref.decode_kv4(q, kp, vp, lens, table)
+    others = [0] + list(range(2, len(lens)))
     for bad in (-1, 201):
-        out = torch.full((3, Hq, 1, D), 5.0, dtype=torch.bfloat16, device="cuda")
-        gqa.attn_decode_kv4(to_dev(q), _dev(kp), _dev(vp), _i32([200, bad, 64]), _i32(table), max_seqlen_k=200, out=out)
+        out = torch.full((len(lens), Hq, 1, D), 5.0, dtype=torch.bfloat16, device="cuda")
+        gqa.attn_decode_kv4(to_dev(q), _dev(kp), _dev(vp), _i32([200, bad] + lens[2:]), _i32(table), max_seqlen_k=200, out=out)
         torch.cuda.synchronize()
         assert gqa.gqa_get_device_error() == gqa.GQA_ERR_INVALID_ARGUMENT
         got = from_dev(out)
         assert (got[1] == 5).all()
-        _near(got[[0, 2]], want[[0, 2]], tol[[0, 2]], "beside a bad length")
+        _near(got[others], want[others], tol[others], "beside a bad length")
 
 
 def test_decode_kv4_nan_stays_with_the_queries_that_see_it(gqa):
