@@ -174,7 +174,7 @@ gqa_status rope_bwd(gqa::RopeParams p, const RopeBwdPlan& r, bool interleaved, f
         gqa::gqa_rope_bwd_kernel<D, false><<<grid, gqa::kRopeThreads, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (dq_weight == nullptr && dk_weight == nullptr)) return launched(e);
-    gqa::gqa_rope_dw_kernel<D><<<dim3(2, D / 32), 1024, 0, stream>>>(p.partial, p.blocks[0] * r.x, r.blocks * r.x, dq_weight,
+    gqa::gqa_rope_dw_kernel<D><<<dim3(2, D / gqa::kRopeDwColumns), 1024, 0, stream>>>(p.partial, p.blocks[0] * r.x, r.blocks * r.x, dq_weight,
                                                                      dk_weight);
     return launched(cudaGetLastError());
 }

@@ -473,23 +473,30 @@ __global__ void __launch_bounds__(kRopeThreads, 2) gqa_rope_bwd_kernel(const __g
     }
 }
 
-// dw[d] = sum of the CTAs' partial sums; blockIdx.x 0: queries, 1: keys; 32 columns a CTA.
+// dw[d] = sum of the CTAs' partial sums; blockIdx.x 0: queries, 1: keys; eight columns a CTA, so
+// that a thread has few rows to wait for.
+constexpr int kRopeDwColumns = 8;
 template <int D>
 __global__ void __launch_bounds__(1024) gqa_rope_dw_kernel(const float* partial, int q_rows, int rows, float* dq_w, float* dk_w) {
-    __shared__ float sums[32][33];
+    constexpr int kGroups = 1024 / kRopeDwColumns;
+    __shared__ float sums[kGroups][kRopeDwColumns + 1];
     float* out = blockIdx.x ? dk_w : dq_w;
     if (out == nullptr) return;
     const int lo = blockIdx.x ? q_rows : 0, hi = blockIdx.x ? rows : q_rows;
-    const int c = threadIdx.x & 31, g = threadIdx.x >> 5, d = blockIdx.y * 32 + c;
+    const int c = threadIdx.x % kRopeDwColumns, g = threadIdx.x / kRopeDwColumns, d = blockIdx.y * kRopeDwColumns + c;
     float v = 0.f;
 #pragma unroll 8
-    for (int i = lo + g; i < hi; i += 32) v += partial[(long long)i * D + d];
+    for (int i = lo + g; i < hi; i += kGroups) v += partial[(long long)i * D + d];
     sums[g][c] = v;
     __syncthreads();
-    v = sums[c][g];  // column g, groups over the lanes
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp >= kRopeDwColumns) return;
+    v = 0.f;
+#pragma unroll
+    for (int i = lane; i < kGroups; i += 32) v += sums[i][warp];
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-    if (c == 0) out[blockIdx.y * 32 + g] = v;
+    if (lane == 0) out[blockIdx.y * kRopeDwColumns + warp] = v;
 }
 
 }  // namespace gqa
