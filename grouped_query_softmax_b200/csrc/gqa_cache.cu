@@ -118,11 +118,11 @@ gqa_status rope_params(gqa::RopeParams& p, const gqa_rope* r, int B, int T, int 
 }
 
 // Heads of a token that one team of D/8 lanes takes in turn: its loads of the angles and weights
-// serve that many rows, so a large launch takes many; a small one takes the four it has in
+// serve that many rows, so a large launch takes `many`; a small one takes the four it has in
 // flight at a time, to spread over the SMs.
-int rope_heads_per_team(long long tokens, int heads, int D, int sms) {
-    const long long lanes_at_16 = tokens * ((heads + 15) / 16) * (D / 8);
-    return lanes_at_16 >= (long long)sms * 2048 ? 16 : gqa::kRopeUnroll;
+int rope_heads_per_team(long long tokens, int heads, int D, int many, int sms) {
+    const long long lanes = tokens * ((heads + many - 1) / many) * (D / 8);
+    return lanes >= (long long)sms * 2048 ? many : gqa::kRopeUnroll;
 }
 // Heads, split into blocks; false if there are more blocks than a grid's y extent.
 bool rope_blocks(gqa::RopeParams& p, int heads_per_team) {
@@ -136,7 +136,7 @@ template <int D>
 gqa_status rope_fwd(gqa::RopeParams p, bool interleaved, cudaStream_t stream) {
     int heads = 0;
     for (int i = 0; i < 3; ++i) heads += p.x[i].H;
-    if (!rope_blocks(p, rope_heads_per_team((long long)p.B * p.T, heads, D, sm_count()))) return GQA_ERR_UNSUPPORTED;
+    if (!rope_blocks(p, rope_heads_per_team((long long)p.B * p.T, heads, D, 16, sm_count()))) return GQA_ERR_UNSUPPORTED;
     if ((p.err = gqa::device_error_ptr()) == nullptr) return GQA_ERR_CUDA;
     constexpr int kPer = gqa::kRopeThreads / (D / 8);
     const dim3 grid((unsigned)(((long long)p.B * p.T + kPer - 1) / kPer), (unsigned)(p.blocks[0] + p.blocks[1] + p.blocks[2]));
@@ -147,8 +147,9 @@ gqa_status rope_fwd(gqa::RopeParams p, bool interleaved, cudaStream_t stream) {
     return launched(cudaGetLastError());
 }
 
-// The backward pass's CTAs: a head block each, over tokens in strides of the grid's x extent, at most
-// eight a SM. Each leaves one row of weight sums.
+// The backward pass's CTAs: a head block each, over tokens in strides of the grid's x extent, as many
+// as run at once (two a SM). Each leaves one row of weight sums. Head blocks of 8 rather than 16
+// divide more head counts evenly, so that the CTAs end together.
 struct RopeBwdPlan {
     int heads_per_team, blocks, x;
 };
@@ -156,9 +157,9 @@ RopeBwdPlan rope_bwd_plan(int B, int T, int Hq, int Hkv, int D) {
     const int sms = sm_count(), per_cta = gqa::kRopeThreads / (D / 8);
     const long long tokens = (long long)B * T;
     RopeBwdPlan r;
-    r.heads_per_team = rope_heads_per_team(tokens, Hq + Hkv, D, sms);
+    r.heads_per_team = rope_heads_per_team(tokens, Hq + Hkv, D, 8, sms);
     r.blocks = (Hq + r.heads_per_team - 1) / r.heads_per_team + (Hkv + r.heads_per_team - 1) / r.heads_per_team;
-    r.x = (int)std::min<long long>((tokens + per_cta - 1) / per_cta, std::max(1, sms * 8 / r.blocks));
+    r.x = (int)std::min<long long>((tokens + per_cta - 1) / per_cta, std::max(1, sms * 2 / r.blocks));
     return r;
 }
 

@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) gqa_rope_bwd_kernel(const __g
     const RopePairs w = rope_weights<kInterleaved>(x.weight, p.weight_fp32, l);
     RopePairs dw;
     dw.a[0] = dw.a[1] = dw.b[0] = dw.b[1] = rope2(0.f, 0.f);
-    const unsigned tokens = (unsigned)p.B * (unsigned)p.T;
-    for (unsigned base = blockIdx.x * kTeams; base < tokens; base += gridDim.x * kTeams) {  // the same for every lane
+    const unsigned tokens = (unsigned)p.B * (unsigned)p.T, stride = gridDim.x * kTeams;
+    for (unsigned base = blockIdx.x * kTeams; base < tokens; base += stride) {  // the same for every lane
         const RopeAt a = rope_at<kLanes>(p, base + team);
         uint64_t c[2], s[2];
         const bool use = rope_angles(p, a, l, c, s) && a.live;
@@ -369,6 +369,18 @@ __global__ void __launch_bounds__(kRopeThreads, 2) gqa_rope_bwd_kernel(const __g
         __nv_bfloat16* out = x.out + a.b * x.out_sb + a.t * x.out_st + a.h0 * x.out_sh + l.e0;
         const int gap = l.e1 - l.e0;
         const bool copy = !norm && l.angle < 0;
+        if (base + stride < tokens) {  // bring the next token's rows to L2
+            const RopeAt next = rope_at<kLanes>(p, base + stride + team);
+            constexpr int kLines = D / 64;  // of 128 bytes in a row
+            const int n = next.live ? (a.h1 - a.h0) * kLines : 0;
+            const __nv_bfloat16* xs = x.in + next.b * x.in_sb + next.t * x.in_st;
+            const __nv_bfloat16* gs = x.grad + next.b * x.grad_sb + next.t * x.grad_st;
+            for (int i = j; i < n; i += kLanes) {
+                const long long h = a.h0 + i / kLines, at = i % kLines * 64;
+                if (norm) asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(xs + h * x.in_sh + at)));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(gs + h * x.grad_sh + at)));
+            }
+        }
         for (int h = a.h0; h < a.h1; h += kUnroll) {
             uint2 x0[kUnroll], x1[kUnroll], g0[kUnroll], g1[kUnroll];
 #pragma unroll
