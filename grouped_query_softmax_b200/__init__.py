@@ -777,12 +777,20 @@ def _attn_fwd_varlen_paged(q, k_pool, v_pool, cu_seqlens_q, seqlens_q, seqlens_k
 
 
 # ---------------------------------------------------------------- around the attention calls
-@functools.lru_cache(maxsize=None)
-def _torch_once():
-    """torch, its dtypes and the current-stream query of the calls below, looked up once."""
-    torch = _torch()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the current stream without a Stream object
-    return torch, raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+class _Torch:
+    """torch's names that the calls below need, looked up on the first of them."""
+    tensor = None
+
+    @classmethod
+    def load(cls):
+        torch = _torch()
+        cls.bf16, cls.f32, cls.i32, cls.u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+        cls.empty, cls.current_device = torch.empty, torch.cuda.current_device
+        # the current stream without a Stream object
+        cls.stream = staticmethod(getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                                  or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+        cls.tensor = torch.Tensor
+        return cls.tensor
 
 
 def _on_device(names, *tensors):
@@ -799,7 +807,7 @@ def _on_device(names, *tensors):
             if device != -2:
                 raise ValueError(f"{names.split()[i]} is on cuda:{d}, the first operand on cuda:{device}")
             device = d
-    if device != _torch_once()[0].cuda.current_device():
+    if device != _Torch.current_device():
         raise ValueError(f"the operands are on cuda:{device}, which is not the current device")
     return device
 
@@ -807,7 +815,7 @@ def _on_device(names, *tensors):
 def _keep_until(stream, *tensors):
     """Tensors allocated here for a call on another stream than the current one stay allocated
     until that stream has passed the call."""
-    torch = _torch_once()[0]
+    torch = _torch()
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
     for t in tensors:
@@ -816,12 +824,11 @@ def _keep_until(stream, *tensors):
 
 
 def _stream_on(stream, device):
-    return _torch_once()[1](device) if stream is None else _stream_handle(stream)
+    return _Torch.stream(device) if stream is None else _stream_handle(stream)
 
 
 def _int32(t, name, shape=None):
-    torch = _torch_once()[0]
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_contiguous():
+    if not isinstance(t, _Torch.tensor or _Torch.load()) or t.dtype is not _Torch.i32 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 tensor")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
@@ -840,12 +847,11 @@ def _c_layout4(sb, sh):
 
 def _bf16_rows(t, name, shape=None, dims=4):
     """Layout of a bf16 operand [B, H, T, D], or [T, H, D] when dims is 3."""
-    torch = _torch_once()[0]
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
+    if not isinstance(t, _Torch.tensor or _Torch.load()) or t.dtype is not _Torch.bf16:
         raise TypeError(f"{name} must be a bf16 tensor")
-    if t.dim() != dims or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must have the shape {tuple(shape) if shape else f'of {dims} axes'}, not {tuple(t.shape)}")
     st = t.stride()
+    if len(st) != dims or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape) if shape else f'of {dims} axes'}, not {tuple(t.shape)}")
     if st[-1] != 1:
         raise ValueError(f"{name}: the last (D) axis must be contiguous")
     return _c_layout(st[0], st[1], st[2]) if dims == 4 else _c_layout(0, st[1], st[0])
@@ -914,35 +920,37 @@ def paged_plan(seqlens, new_tokens, block_table, free_list, free_count, *, page_
 
 def _rope_args(D, B, T, q_weight, k_weight, eps, cos, sin, positions, interleaved):
     """The GqaRope of a call."""
-    torch = _torch_once()[0]
-    weight = k_weight if q_weight is None else q_weight
-    if weight is not None:
-        for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-            if w is None:
-                continue
-            if w.dtype not in (torch.bfloat16, torch.float32) or w.shape != (D,) or not w.is_contiguous():
-                raise TypeError(f"{n} must be a contiguous bf16 or fp32 tensor [{D}]")
-            if w.dtype is not weight.dtype:
-                raise TypeError("q_weight and k_weight must have the same type")
+    q_ptr = k_ptr = cos_ptr = sin_ptr = pos_ptr = None
+    fp32 = pos_sb = rows = rot = 0
+    if q_weight is not None:
+        q_ptr, fp32 = q_weight.data_ptr(), q_weight.dtype is _Torch.f32
+        if q_weight.shape != (D,) or not q_weight.is_contiguous() or not (fp32 or q_weight.dtype is _Torch.bf16):
+            raise TypeError(f"q_weight must be a contiguous bf16 or fp32 tensor [{D}]")
+    if k_weight is not None:
+        k_ptr, k_fp32 = k_weight.data_ptr(), k_weight.dtype is _Torch.f32
+        if k_weight.shape != (D,) or not k_weight.is_contiguous() or not (k_fp32 or k_weight.dtype is _Torch.bf16):
+            raise TypeError(f"k_weight must be a contiguous bf16 or fp32 tensor [{D}]")
+        if q_weight is not None and k_fp32 is not fp32:
+            raise TypeError("q_weight and k_weight must have the same type")
+        fp32 = k_fp32
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
-    pos_ptr = pos_sb = 0
-    if cos is None:
-        if positions is not None:
-            raise ValueError("positions need cos and sin")
-        tables = (None, None, None, 0, 0, 0)
-    else:
-        for n, t in (("cos", cos), ("sin", sin)):
-            if t.dtype is not torch.float32 or t.dim() != 2 or t.shape != cos.shape or not t.is_contiguous():
-                raise TypeError(f"{n} must be a contiguous fp32 tensor [positions, rot / 2]")
+    if cos is not None:
+        shape = cos.shape
+        if (len(shape) != 2 or sin.shape != shape or cos.dtype is not _Torch.f32 or sin.dtype is not _Torch.f32
+                or not cos.is_contiguous() or not sin.is_contiguous()):
+            raise TypeError("cos and sin must be contiguous fp32 tensors [positions, rot / 2]")
+        cos_ptr, sin_ptr, rows, rot = cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1]
         if positions is not None:
             _int32(positions, "positions")
-            if positions.shape != (T,) and positions.shape != (B, T):
-                raise ValueError(f"positions must be [{T}] or [{B}, {T}]")
-            pos_ptr, pos_sb = positions.data_ptr(), T if positions.dim() == 2 else 0
-        tables = (cos.data_ptr(), sin.data_ptr(), pos_ptr, pos_sb, cos.shape[0], 2 * cos.shape[1])
-    return GqaRope(None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
-                   *tables, bool(interleaved), weight is not None and weight.dtype is torch.float32, eps)
+            if positions.shape != (T,):
+                if positions.shape != (B, T):
+                    raise ValueError(f"positions must be [{T}] or [{B}, {T}]")
+                pos_sb = T
+            pos_ptr = positions.data_ptr()
+    elif positions is not None:
+        raise ValueError("positions need cos and sin")
+    return GqaRope(q_ptr, k_ptr, cos_ptr, sin_ptr, pos_ptr, pos_sb, rows, rot, bool(interleaved), fp32, eps)
 
 
 _ROPE_NAMES = " q_weight k_weight cos sin positions"
@@ -987,7 +995,6 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, *, q_weight=None, k_weight=None, eps=
     """Gradients (dq, dk, dq_weight, dk_weight) of ``qk_norm_rope(q, k, ...)`` for the gradients of
     its outputs (for instance ``attn_bwd``'s dq and dk). The weights' gradients are fp32 [D], None
     for a side without a weight. dq and dk may be dq_out and dk_out themselves."""
-    torch = _torch_once()[0]
     lq = _bf16_rows(q, "q")
     B, Hq, T, D = q.shape
     lk = _bf16_rows(k, "k")
@@ -1008,7 +1015,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, *, q_weight=None, k_weight=None, eps=
         if workspace is None:
             need = gqa_qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hkv, D)
         # one allocation: the weights' gradients behind the workspace
-        buf = torch.empty(need // 4 + 2 * D, dtype=torch.float32, device=q.device)
+        buf = _Torch.empty(need // 4 + 2 * D, dtype=_Torch.f32, device=q.device)
         fresh.append(buf)
         ws_ptr, ws_bytes = buf.data_ptr(), need
         if workspace is not None:
@@ -1078,15 +1085,14 @@ def qk_norm_rope_append(q, k, v, k_pool, v_pool, slots, *, q_weight=None, k_weig
 
 def kv4_pool(num_pages, num_heads, page_size, D, device=None):
     """A pool of zero rows for a paged cache held in 4 bits: uint8 [pages, Hkv, page, D / 2 + 4]."""
-    torch = _torch_once()[0]
+    torch = _torch()
     return torch.zeros((num_pages, num_heads, page_size, D // 2 + 4), dtype=torch.uint8,
                        device=torch.cuda.current_device() if device is None else device)
 
 
 def _kv4_layout(t, name, D, shape=None):
     """Layout of a 4-bit pool [pages, Hkv, page, D / 2 + 4]."""
-    torch = _torch_once()[0]
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8:
+    if not isinstance(t, _Torch.tensor or _Torch.load()) or t.dtype is not _Torch.u8:
         raise TypeError(f"{name} must be a uint8 tensor")
     if t.dim() != 4 or t.shape[3] != D // 2 + 4 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must be [pages, Hkv, page, {D // 2 + 4}] (both pools alike), not {tuple(t.shape)}")
@@ -1117,8 +1123,7 @@ def kv4_append(k, v, k_pool, v_pool, slots, *, stream=None):
 def kv4_gather(k_pool, v_pool, slots, *, k=None, v=None, stream=None):
     """Rows ``slots`` (int32 [N]) of the 4-bit pools as bf16 (k, v) [N, Hkv, D]; a slot outside
     the pool gives zeros."""
-    torch = _torch_once()[0]
-    if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
+    if not isinstance(k_pool, _Torch.tensor or _Torch.load()) or k_pool.dim() != 4:
         raise TypeError("k_pool must be a uint8 tensor [pages, Hkv, page, D / 2 + 4]")
     pages, Hkv, page, row = k_pool.shape
     D = 2 * (row - 4)
@@ -1128,10 +1133,10 @@ def kv4_gather(k_pool, v_pool, slots, *, k=None, v=None, stream=None):
     device = _on_device("k_pool v_pool slots k v", k_pool, v_pool, slots, k, v)
     fresh = None
     if k is None and v is None:
-        fresh = torch.empty((2, N, Hkv, D), dtype=torch.bfloat16, device=k_pool.device)
+        fresh = _Torch.empty((2, N, Hkv, D), dtype=_Torch.bf16, device=k_pool.device)
         k, v = fresh.unbind(0)
     elif k is None or v is None:
-        fresh = torch.empty((N, Hkv, D), dtype=torch.bfloat16, device=k_pool.device)
+        fresh = _Torch.empty((N, Hkv, D), dtype=_Torch.bf16, device=k_pool.device)
         k, v = (fresh, v) if k is None else (k, fresh)
     st = _lib.gqa_kv4_gather(k_pool.data_ptr(), v_pool.data_ptr(), k.data_ptr(), v.data_ptr(), slots.data_ptr(), N, Hkv, D,
                              page, pages, sk, sv, _bf16_rows(k, "k", (N, Hkv, D), dims=3),
@@ -1152,8 +1157,7 @@ def attn_decode_kv4(q, k_pool, v_pool, seqlens_k, block_table, *, max_seqlen_k=N
     [B, max_pages]. ``workspace``: a uint8 CUDA tensor of gqa_attn_decode_kv4_workspace_bytes(...)
     bytes, allocated here when omitted.
     """
-    torch = _torch_once()[0]
-    if not isinstance(q, torch.Tensor) or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.dim() not in (3, 4):
+    if not isinstance(q, _Torch.tensor or _Torch.load()) or q.dtype is not _Torch.bf16 or not q.is_contiguous() or q.dim() not in (3, 4):
         raise TypeError("q must be a contiguous bf16 tensor [B, Hq, Tq, D] or [B, Hq, D]")
     B, Hq, D = q.shape[0], q.shape[1], q.shape[-1]
     Tq = q.shape[2] if q.dim() == 4 else 1
@@ -1171,12 +1175,12 @@ def attn_decode_kv4(q, k_pool, v_pool, seqlens_k, block_table, *, max_seqlen_k=N
     fresh_out = fresh_ws = None
     if out is None:
         out = fresh_out = q.new_empty(q.shape)
-    elif out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
+    elif out.dtype is not _Torch.bf16 or out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 tensor shaped like q")
     if workspace is None:
         need = _lib.gqa_attn_decode_kv4_workspace_bytes(B, Hq, Hkv, Tq, max_seqlen_k, D, window)
         if need:
-            workspace = fresh_ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = fresh_ws = _Torch.empty(need, dtype=_Torch.u8, device=q.device)
     st = _lib.gqa_attn_decode_kv4(q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), out.data_ptr(), seqlens_k.data_ptr(),
                                   block_table.data_ptr(), page, pages, max_pages, B, Hq, Hkv, Tq, max_seqlen_k, D, sk, sv,
                                   float(scale or 0.0), window, _ptr(workspace),
