@@ -147,19 +147,23 @@ gqa_status rope_fwd(gqa::RopeParams p, bool interleaved, cudaStream_t stream) {
     return launched(cudaGetLastError());
 }
 
-// The backward pass's CTAs: a head block each, over tokens in strides of the grid's x extent, as many
-// as run at once (two a SM). Each leaves one row of weight sums. Head blocks of 8 rather than 16
-// divide more head counts evenly, so that the CTAs end together.
+// The backward pass's CTAs: as many as run at once (two a SM), or as there is work for, dealt to the
+// operands in proportion to their heads in fours. Each leaves one row of weight sums.
 struct RopeBwdPlan {
-    int heads_per_team, blocks, x;
+    int heads_per_team, q_ctas, ctas;
 };
 RopeBwdPlan rope_bwd_plan(int B, int T, int Hq, int Hkv, int D) {
     const int sms = sm_count(), per_cta = gqa::kRopeThreads / (D / 8);
-    const long long tokens = (long long)B * T;
+    const long long groups = ((long long)B * T + per_cta - 1) / per_cta;
     RopeBwdPlan r;
-    r.heads_per_team = rope_heads_per_team(tokens, Hq + Hkv, D, 8, sms);
-    r.blocks = (Hq + r.heads_per_team - 1) / r.heads_per_team + (Hkv + r.heads_per_team - 1) / r.heads_per_team;
-    r.x = (int)std::min<long long>((tokens + per_cta - 1) / per_cta, std::max(1, sms * 2 / r.blocks));
+    r.heads_per_team = rope_heads_per_team((long long)B * T, Hq + Hkv, D, 8, sms);
+    const auto fours = [](int H) { return (H + gqa::kRopeUnroll - 1) / gqa::kRopeUnroll; };  // a lane's steps
+    const auto ctas = [&](int H) {
+        const long long units = groups * ((H + r.heads_per_team - 1) / r.heads_per_team);
+        return (int)std::min<long long>(units, std::max<long long>(1, 2LL * sms * fours(H) / (fours(Hq) + fours(Hkv))));
+    };
+    r.q_ctas = ctas(Hq);
+    r.ctas = r.q_ctas + ctas(Hkv);
     return r;
 }
 
@@ -168,14 +172,15 @@ gqa_status rope_bwd(gqa::RopeParams p, const RopeBwdPlan& r, bool interleaved, f
                     cudaStream_t stream) {
     if (!rope_blocks(p, r.heads_per_team)) return GQA_ERR_UNSUPPORTED;
     if ((p.err = gqa::device_error_ptr()) == nullptr) return GQA_ERR_CUDA;
-    const dim3 grid((unsigned)r.x, (unsigned)r.blocks);
+    p.q_ctas = r.q_ctas;
+    const unsigned grid = (unsigned)r.ctas;
     if (interleaved)
         gqa::gqa_rope_bwd_kernel<D, true><<<grid, gqa::kRopeThreads, 0, stream>>>(p);
     else
         gqa::gqa_rope_bwd_kernel<D, false><<<grid, gqa::kRopeThreads, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (dq_weight == nullptr && dk_weight == nullptr)) return launched(e);
-    gqa::gqa_rope_dw_kernel<D><<<dim3(2, D / gqa::kRopeDwColumns), 1024, 0, stream>>>(p.partial, p.blocks[0] * r.x, r.blocks * r.x, dq_weight,
+    gqa::gqa_rope_dw_kernel<D><<<dim3(2, D / gqa::kRopeDwColumns), 1024, 0, stream>>>(p.partial, r.q_ctas, r.ctas, dq_weight,
                                                                      dk_weight);
     return launched(cudaGetLastError());
 }
@@ -414,7 +419,7 @@ gqa_status gqa_qk_norm_rope_append(const void* q, const void* k, const void* v, 
 size_t gqa_qk_norm_rope_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
     if (check_heads(Hq, Hkv, D) != GQA_OK || B <= 0 || T <= 0) return 0;
     const RopeBwdPlan r = rope_bwd_plan(B, T, Hq, Hkv, D);
-    return gqa::round256((size_t)r.blocks * r.x * D * sizeof(float));
+    return gqa::round256((size_t)r.ctas * D * sizeof(float));
 }
 
 gqa_status gqa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, void* dq, void* dk,

@@ -57,8 +57,9 @@ struct RopeParams {
     const int* slots;  // [T], or null: not appending
     int page_size, num_pages;
     int heads_per_team;  // rows of one token that a team takes in turn
-    int blocks[3];       // head blocks of each operand; gridDim.y is their sum
-    float* partial;      // backward: [gridDim.y, gridDim.x, D] sums of dw
+    int blocks[3];       // head blocks of each operand; forward: gridDim.y is their sum
+    float* partial;      // backward: [gridDim.x, D] sums of dw
+    int q_ctas;          // backward: CTAs that take queries, the first ones
     uint32_t* err;
 };
 
@@ -209,18 +210,15 @@ struct RopeAt {
     bool live;
     int b, t, which, h0, h1;
 };
-template <int kLanes>
-__device__ __forceinline__ RopeAt rope_at(const RopeParams& p, unsigned tok) {
+__device__ __forceinline__ RopeAt rope_at(const RopeParams& p, unsigned tok, int which, int hb) {
     RopeAt a;
+    a.which = which;
     a.live = tok < (unsigned)p.B * (unsigned)p.T;  // every lane stays for the exchanges
     if (!a.live) tok = 0;
     a.b = p.B == 1 ? 0 : (int)(tok / (unsigned)p.T);
     a.t = (int)(tok - (unsigned)a.b * (unsigned)p.T);
-    int hb = blockIdx.y;
-    a.which = hb < p.blocks[0] ? 0 : hb < p.blocks[0] + p.blocks[1] ? 1 : 2;
-    hb -= a.which == 0 ? 0 : a.which == 1 ? p.blocks[0] : p.blocks[0] + p.blocks[1];
     a.h0 = hb * p.heads_per_team;
-    a.h1 = min(a.h0 + p.heads_per_team, p.x[a.which].H);
+    a.h1 = min(a.h0 + p.heads_per_team, p.x[which].H);
     return a;
 }
 // The angles of a team's token in the lane's four pairs (1, 0 where nothing turns); false, with
@@ -251,7 +249,10 @@ __global__ void __launch_bounds__(kRopeThreads, 4) gqa_rope_fwd_kernel(const __g
     constexpr int kLanes = D / 8;
     constexpr int kUnroll = kRopeUnroll;
     const int j = threadIdx.x % kLanes;
-    const RopeAt a = rope_at<kLanes>(p, blockIdx.x * (kRopeThreads / kLanes) + threadIdx.x / kLanes);
+    int hb = blockIdx.y;
+    const int which = hb < p.blocks[0] ? 0 : hb < p.blocks[0] + p.blocks[1] ? 1 : 2;
+    hb -= which == 0 ? 0 : which == 1 ? p.blocks[0] : p.blocks[0] + p.blocks[1];
+    const RopeAt a = rope_at(p, blockIdx.x * (kRopeThreads / kLanes) + threadIdx.x / kLanes, which, hb);
     const RopeRows& x = p.x[a.which];
     const RopeLane l = rope_lane<D, kInterleaved>(j, p.rot);
 
@@ -340,9 +341,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4) gqa_rope_fwd_kernel(const __g
     }
 }
 
-// Backward. A CTA takes one head block (blockIdx.y) of a strided share of the tokens, and leaves one
-// row of dw sums; gqa_rope_dw_kernel adds those up in a fixed order, so the gradients do not
-// change from run to run.
+// Backward. A CTA takes one operand's rows, a strided share of its (token group, head block)s, and
+// leaves one row of dw sums; gqa_rope_dw_kernel adds those up in a fixed order, so the gradients do
+// not change from run to run. The operands get CTAs in proportion to their heads.
 //   g = R^T dz,  dw += (g x) r,  dx = (r g) w - x (r^3 sum(g w x) / D)
 template <int D, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, 2) gqa_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
@@ -352,15 +353,20 @@ __global__ void __launch_bounds__(kRopeThreads, 2) gqa_rope_bwd_kernel(const __g
     __shared__ float sums[kTeams][D];
     const int j = threadIdx.x % kLanes, team = threadIdx.x / kLanes;
     const RopeLane l = rope_lane<D, kInterleaved>(j, p.rot);
-    const RopeAt first = rope_at<kLanes>(p, 0);
-    const RopeRows& x = p.x[first.which];
+    const int which = (int)blockIdx.x < p.q_ctas ? 0 : 1;
+    const RopeRows& x = p.x[which];
     const bool norm = x.weight != nullptr;
     const RopePairs w = rope_weights<kInterleaved>(x.weight, p.weight_fp32, l);
     RopePairs dw;
     dw.a[0] = dw.a[1] = dw.b[0] = dw.b[1] = rope2(0.f, 0.f);
-    const unsigned tokens = (unsigned)p.B * (unsigned)p.T, stride = gridDim.x * kTeams;
-    for (unsigned base = blockIdx.x * kTeams; base < tokens; base += stride) {  // the same for every lane
-        const RopeAt a = rope_at<kLanes>(p, base + team);
+    const unsigned blocks = p.blocks[which], units = ((unsigned)p.B * (unsigned)p.T + kTeams - 1) / kTeams * blocks;
+    const unsigned stride = which ? gridDim.x - p.q_ctas : p.q_ctas;
+    const auto place = [&](unsigned u) {  // of this team in unit u
+        const unsigned group = u / blocks;
+        return rope_at(p, group * kTeams + team, which, (int)(u - group * blocks));
+    };
+    for (unsigned u = which ? blockIdx.x - p.q_ctas : blockIdx.x; u < units; u += stride) {  // the same for every lane
+        const RopeAt a = place(u);
         uint64_t c[2], s[2];
         const bool use = rope_angles(p, a, l, c, s) && a.live;
         const uint64_t ns[2] = {rope2_neg(s[0]), rope2_neg(s[1])};
@@ -369,14 +375,14 @@ __global__ void __launch_bounds__(kRopeThreads, 2) gqa_rope_bwd_kernel(const __g
         __nv_bfloat16* out = x.out + a.b * x.out_sb + a.t * x.out_st + a.h0 * x.out_sh + l.e0;
         const int gap = l.e1 - l.e0;
         const bool copy = !norm && l.angle < 0;
-        if (base + stride < tokens) {  // bring the next token's rows to L2
-            const RopeAt next = rope_at<kLanes>(p, base + stride + team);
+        if (u + stride < units) {  // bring the next unit's rows to L2
+            const RopeAt next = place(u + stride);
             constexpr int kLines = D / 64;  // of 128 bytes in a row
-            const int n = next.live ? (a.h1 - a.h0) * kLines : 0;
+            const int n = next.live ? (next.h1 - next.h0) * kLines : 0;
             const __nv_bfloat16* xs = x.in + next.b * x.in_sb + next.t * x.in_st;
             const __nv_bfloat16* gs = x.grad + next.b * x.grad_sb + next.t * x.grad_st;
             for (int i = j; i < n; i += kLanes) {
-                const long long h = a.h0 + i / kLines, at = i % kLines * 64;
+                const long long h = next.h0 + i / kLines, at = i % kLines * 64;
                 if (norm) asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(xs + h * x.in_sh + at)));
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(gs + h * x.grad_sh + at)));
             }
@@ -481,7 +487,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) gqa_rope_bwd_kernel(const __g
         float v = 0.f;
 #pragma unroll
         for (int i = 0; i < kTeams; ++i) v += sums[i][threadIdx.x];
-        p.partial[((long long)blockIdx.y * gridDim.x + blockIdx.x) * D + threadIdx.x] = v;
+        p.partial[(long long)blockIdx.x * D + threadIdx.x] = v;
     }
 }
 
