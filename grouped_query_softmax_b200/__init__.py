@@ -898,9 +898,13 @@ def paged_plan(seqlens, new_tokens, block_table, free_list, free_count, *, page_
     if out is None:
         if max_tokens <= 0:
             raise ValueError("max_tokens must be positive")
-        pad = -max_tokens % 4  # positions and slots start on 16 bytes
-        fresh = seqlens.new_empty(2 * (max_tokens + pad) + 2 * S + 2)
-        pos, _, slots, _, cu, lens, count = fresh.split_with_sizes((max_tokens, pad, max_tokens, pad, S + 1, S, 1))
+        # one allocation; positions and slots start on 16 bytes
+        pad = -(max_tokens + 2 * S + 2) % 4
+        fresh = seqlens.new_empty(2 * max_tokens + 2 * S + 2 + pad)
+        if pad:
+            pos, lens, cu, count, _, slots = fresh.split_with_sizes((max_tokens, S, S + 1, 1, pad, max_tokens))
+        else:
+            pos, lens, cu, count, slots = fresh.split_with_sizes((max_tokens, S, S + 1, 1, max_tokens))
         out = PagedPlan(lens, cu, pos, slots, count)
     else:
         for t, n, shape in zip(out, PagedPlan._fields, ((S,), (S + 1,), (max_tokens,), (max_tokens,), (1,))):

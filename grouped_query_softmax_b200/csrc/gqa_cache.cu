@@ -79,7 +79,7 @@ gqa_status paged_plan(const gqa::PagedPlanParams& p, cudaStream_t stream) {
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = kCluster ? 1 : 0;
     return launched(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
@@ -171,6 +171,7 @@ template <int D>
 gqa_status rope_bwd(gqa::RopeParams p, const RopeBwdPlan& r, bool interleaved, float* dq_weight, float* dk_weight,
                     cudaStream_t stream) {
     if (!rope_blocks(p, r.heads_per_team)) return GQA_ERR_UNSUPPORTED;
+    if ((long long)p.B * p.T * p.blocks[0] > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;  // units in 32 bits
     if ((p.err = gqa::device_error_ptr()) == nullptr) return GQA_ERR_CUDA;
     p.q_ctas = r.q_ctas;
     const unsigned grid = (unsigned)r.ctas;
@@ -318,7 +319,7 @@ gqa_status launch_dec4(const gqa::Dec4Params& p, const Dec4Plan& r, cudaStream_t
     if (e != cudaSuccess) return GQA_ERR_CUDA;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = r.cluster ? r.cluster : 1;
+    attr.val.clusterDim.x = r.cluster;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)r.ctas);
@@ -326,7 +327,7 @@ gqa_status launch_dec4(const gqa::Dec4Params& p, const Dec4Plan& r, cudaStream_t
     cfg.dynamicSmemBytes = C::kBytes;
     cfg.stream = stream;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = r.cluster ? 1 : 0;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess || r.cluster) return launched(e);
     const dim3 grid((unsigned)p.B, (unsigned)(p.Hq * p.Tq));
     gqa::gqa_decode_kv4_merge_kernel<D, NT><<<grid, 32 * gqa::kD4MergeWarps, 0, stream>>>(p);
@@ -353,7 +354,8 @@ gqa_status gqa_paged_plan(const int* seqlens, const int* keep, const int* new_to
                            positions, slots,   free_count_out, S,       max_pages,  page_size,  num_pages,   free_capacity,
                            max_tokens, gqa::device_error_ptr()};
     if (p.err == nullptr) return GQA_ERR_CUDA;
-    const bool in_place = seqlens_out == seqlens || free_count_out == free_count;
+    const bool in_place =
+        seqlens_out == seqlens || seqlens_out == keep || seqlens_out == new_tokens || free_count_out == free_count;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (S <= gqa::kPagedFewSeqs) return in_place ? paged_plan<gqa::kPagedFewSeqs, true>(p, s) : paged_plan<gqa::kPagedFewSeqs, false>(p, s);
     return in_place ? paged_plan<1024, true>(p, s) : paged_plan<1024, false>(p, s);

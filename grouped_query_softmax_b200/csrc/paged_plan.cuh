@@ -11,8 +11,8 @@
 // memory; the work after the scan is shared out. Nothing is read and written at once: pops read the
 // list below free_count, pushes write it from free_count on (a popped page that this call released
 // is looked up in the table it came from, not in the list), and a request that releases pages
-// takes none. Only where seqlens_out is seqlens, or free_count_out free_count, must every CTA have
-// read them before one writes: then the CTAs are one cluster with a barrier in between, else they
+// takes none. Only where seqlens_out is one of the inputs, or free_count_out is free_count, must every
+// CTA have read them before one writes: then the CTAs are one cluster with a barrier in between, else they
 // are as many as there is work for and need none. Calling again with the same seqlens and
 // free_count gives the same result.
 //

@@ -422,7 +422,7 @@ GQA_API gqa_status gqa_attn_bwd(const void* q, const void* k, const void* v, con
  *                  entries of the pages it takes are written, others keep what they hold.
  *   free_list      int32 [free_capacity]; entries at and past the new count keep what they hold.
  *   free_count     int32 [1]; free_count_out int32 [1], may be free_count itself.
- *   seqlens_out    int32 [S], may be seqlens itself.
+ *   seqlens_out    int32 [S], may be seqlens, keep or new_tokens itself.
  *   cu_seqlens     int32 [S + 1]: token t of the step belongs to the request s with
  *                  cu[s] <= t < cu[s + 1] (the cu_seqlens_q of gqa_attn_fwd_varlen_paged).
  *   positions, slots  int32 [max_tokens], 16-byte aligned: the token's position in its request
@@ -549,8 +549,10 @@ GQA_API gqa_status gqa_kv4_gather(const void* k_pool, const void* v_pool, void* 
  * gqa_attn_decode_varlen over a cache held in 4 bits: q, o bf16 [B, Hq, Tq, D] contiguous,
  * 1 <= Tq <= 16; sequence b's queries sit at positions L(b) - Tq .. L(b) - 1, L(b) =
  * seqlens_k[b]; block_table int32 [B, max_pages] as there.
- *   Scores, softmax and sums are fp32; the stored rows enter exactly, and the product of a
- *   probability and a value row's step is rounded to bf16 (as P is in the other calls).
+ *   Scores, softmax and sums are fp32, and the stored rows enter exactly. The product of a
+ *   probability and a value row's step is rounded to fp16, relative to the largest step among
+ *   the rows it is summed with: below 2^-28 of that it loses bits, below 2^-39 it vanishes.
+ *   q and the steps are below 2^117 in size (or NaN, which stays with the queries that see it).
  *   Every L(b) must lie in [0, min(max_seqlen_k, max_pages * page_size)], max_seqlen_k <= 2^30.
  *   A query at a negative position (L(b) < Tq) sees no key and gets zeros. A sequence outside
  *   that range gets no output and is reported by the next gqa_get_device_error().

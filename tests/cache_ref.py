@@ -145,9 +145,11 @@ def kv4_values(rows):
 def decode_kv4(q, k_pool, v_pool, lens, table, window=0, scale=None):
     """(o, largest error a right kernel can make) of q [B, Hq, Tq, D] bf16 bits, pools uint8.
 
-    Error: the output's rounding to bf16 (2^-8 of it); the rounding of p * s to bf16 (2^-8 of
-    sum p s |code - 8|, the codes being summed about 8); fp32 sums and exponentials, 2^-13 of
-    sum p |v| (a score's error is at most 2^-22 * scale * s * 31 sum|q|, under 2^-14 here)."""
+    Error: the output's rounding to bf16, 2^-8 of it. The rounding of w = p * s to fp16, 2^-11 of
+    sum w |code - 8| (the codes are summed about 8). fp32 sums of w * code: one rounding each 16
+    keys, 2^-24 of at most 15 sum w, so 2^-10 of sum w up to 16000 keys. Scores: products of
+    codes are exact and eight fp32 sums of 16 of them are off by 2^-21 * scale * s * 15 sum|q|, under
+    2^-15 for these inputs, and the exponentials by 2^-21 more: 2^-13 of sum p |v|."""
     q = f64(q)
     B, Hq, Tq, D = q.shape
     pages, Hkv, page, _ = k_pool.shape
@@ -176,6 +178,6 @@ def decode_kv4(q, k_pool, v_pool, lens, table, window=0, scale=None):
                 p /= p.sum()
                 v = vc[see, h] * vs[see, h] + vm[see, h]
                 out[b, a, i] = p @ v
-                tol[b, a, i] = (2.0 ** -8 * np.abs(out[b, a, i]) + 2.0 ** -8 * (p @ (vs[see, h] * np.abs(vc[see, h] - 8)))
-                                + 2.0 ** -13 * (p @ np.abs(v)))
+                tol[b, a, i] = (2.0 ** -8 * np.abs(out[b, a, i]) + 2.0 ** -11 * (p @ (vs[see, h] * np.abs(vc[see, h] - 8)))
+                                + 2.0 ** -10 * (p @ vs[see, h]) + 2.0 ** -13 * (p @ np.abs(v)))
     return out, tol

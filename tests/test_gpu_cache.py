@@ -450,7 +450,7 @@ def test_decode_kv4_strided_pools_scale_and_bad_pages(gqa):
     o = gqa.attn_decode_kv4(to_dev(q), big[:, 1, 0], big[:, 1, 1], _i32(lens), _i32(table), scale=0.3)
     _sync_ok(gqa)
     want, tol = ref.decode_kv4(q[:, :, None], kp, vp, lens, table, scale=0.3)
-    _near(from_dev(o), want[:, :, 0], 2 * tol[:, :, 0], "strided")   # scale 0.3: scores' error grows by 3.4 x 2^-14
+    _near(from_dev(o), want[:, :, 0], 2 * tol[:, :, 0], "strided")   # scale 0.3: the scores' error is 3.4 times as large
 
 
 @pytest.mark.parametrize("extra", [0, 230])
@@ -483,6 +483,38 @@ def test_decode_kv4_nan_stays_with_the_queries_that_see_it(gqa):
     bad = np.isnan(got).all(-1)[0]
     assert bad[:2].tolist() == [[False, False, True, True]] * 2 and bad[2:].tolist() == [[False, False, False, True]] * 2
     assert np.isfinite(got[0][~bad]).all()
+
+
+def test_offsets_past_32_bits(gqa):
+    """Pools of more than 2^32 bytes (4-bit rows) and 2^31 elements (bf16): rows on the last pages."""
+    torch = torch_mod()
+    Hkv, D, page, N = 8, 128, 64, 200
+    pages = (1 << 32) // (Hkv * page * 68) + 40
+    slots = (pages - 1 - np.arange(N) // page) * page + np.arange(N) % page
+    k, v = gi.normal_bf16(91, 1, (N, Hkv, D)), gi.normal_bf16(92, 2, (N, Hkv, D))
+    pools = [torch.empty((pages, Hkv, page, 68), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    gqa.kv4_append(to_dev(k), to_dev(v), *pools, _i32(slots))
+    back = gqa.kv4_gather(*pools, _i32(slots))
+    lens, table = [N], np.array([[pages - 1 - i for i in range(4)]])
+    q = gi.normal_bf16(93, 0, (1, 32, D))
+    o = gqa.attn_decode_kv4(to_dev(q), *pools, _i32(lens), _i32(table))
+    _sync_ok(gqa)
+    for b, x in zip(back, (k, v)):
+        want = gi.bf16_bits_to_f32(ref.bf16_bits(ref.kv4_values(ref.kv4_pack(x)[0]).astype(np.float32)))
+        np.testing.assert_array_equal(from_dev(b), want.reshape(x.shape))
+    tail = [p[-4:].cpu().numpy() for p in pools]
+    want, tol = ref.decode_kv4(q[:, :, None], *tail, lens, table - (pages - 4))
+    _near(from_dev(o), want[:, :, 0], tol[:, :, 0], "last pages")
+    del pools
+    pages = (1 << 31) // (Hkv * page * D) + 10
+    pool = torch.empty((2, pages, page, Hkv, D), dtype=torch.bfloat16, device="cuda")
+    slots = (pages - 1 - np.arange(N) // page) * page + np.arange(N) % page
+    kd, vd = to_dev(k), to_dev(v)
+    got = gqa.qk_norm_rope_append(kd, kd, vd, pool[0], pool[1], _i32(slots))
+    _sync_ok(gqa)
+    at = torch.tensor(slots, device="cuda")
+    assert torch.equal(got, kd)
+    assert torch.equal(pool[0][at // page, at % page], kd) and torch.equal(pool[1][at // page, at % page], vd)
 
 
 # ---------------------------------------------------------------- together
@@ -607,6 +639,40 @@ def test_training_step_gradients(gqa):
         err = np.abs(from_dev(got[i]) - dx)
         assert err.max() <= 2.0 ** -5 * np.abs(dx).max() and err.mean() <= 2.0 ** -7 * np.abs(dx).mean()
         assert np.abs(got[2 + i].cpu().numpy() - dw).max() <= 2.0 ** -6 * wsize.max()
+
+
+@pytest.mark.parametrize("B", [3, 90])
+def test_decode_kv4_captured_and_replayed(gqa, B):
+    """One graph, lengths and queries changed between replays (a cluster a unit; runs of tiles), beside
+    a second graph with a workspace of its own on another stream."""
+    torch = torch_mod()
+    kp, vp, table = _kv4_pools([400] * B, 4, 64, 32, 85)
+    q = torch.zeros(B, 8, 1, 64, dtype=torch.bfloat16, device="cuda")
+    lens = _i32([400] * B)
+    args = (_dev(kp), _dev(vp), lens, _i32(table))
+    graphs = []
+    side = torch.cuda.Stream()
+    gqa.attn_decode_kv4(q, *args)   # before the capture
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = gqa.attn_decode_kv4(q, *args, max_seqlen_k=400)
+        graphs.append((g, out))
+    for step in range(3):
+        n = gi.uniform_ints(86 + step, gi.STREAM_LEN, B, 0, 400)
+        bits = gi.normal_bf16(87 + step, 0, (B, 8, 1, 64))
+        lens.copy_(_i32(n))
+        q.copy_(to_dev(bits))
+        for g, out in graphs:
+            out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graphs[0][0].replay()
+        graphs[1][0].replay()
+        _sync_ok(gqa)
+        want, tol = ref.decode_kv4(bits, kp, vp, n, table)
+        for g, out in graphs:
+            _near(from_dev(out), want, tol, f"replay {step}")
 
 
 def test_two_streams_at_once_and_foreign_operands(gqa):
