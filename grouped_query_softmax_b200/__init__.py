@@ -785,7 +785,8 @@ class _Torch:
     def load(cls):
         torch = _torch()
         cls.bf16, cls.f32, cls.i32, cls.u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-        cls.empty, cls.current_device = torch.empty, torch.cuda.current_device
+        cls.empty, cls.empty_like, cls.rows = torch.empty, torch.empty_like, torch.contiguous_format
+        cls.current_device = torch.cuda.current_device
         # the current stream without a Stream object
         cls.stream = staticmethod(getattr(torch._C, "_cuda_getCurrentRawStream", None)
                                   or (lambda device: torch.cuda.current_stream(device).cuda_stream))
@@ -843,6 +844,14 @@ def _c_layout(sb, sh, st):
 @functools.lru_cache(maxsize=4096)
 def _c_layout4(sb, sh):
     return GqaKv4Layout(sb, sh)
+
+
+def _fresh_rows(like):
+    """A contiguous tensor like the given one, [B, H, T, D] or [T, H, D], and its layout."""
+    shape = like.shape
+    D = shape[-1]
+    lay = _c_layout(shape[1] * shape[2] * D, shape[2] * D, D) if len(shape) == 4 else _c_layout(0, D, shape[1] * D)
+    return _Torch.empty_like(like, memory_format=_Torch.rows), lay
 
 
 def _bf16_rows(t, name, shape=None, dims=4):
@@ -979,18 +988,23 @@ def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, eps=1e-6, cos=None, sin=
         raise ValueError("q and k must be [B, Hq, T, D] and [B, Hkv, T, D]")
     r = _rope_args(D, B, T, q_weight, k_weight, eps, cos, sin, positions, interleaved)
     device = _on_device("q k q_out k_out" + _ROPE_NAMES, q, k, q_out, k_out, q_weight, k_weight, cos, sin, positions)
-    fresh_q = fresh_k = None
+    fresh = []
     if q_out is None:
-        q_out = fresh_q = q.new_empty(q.shape)
+        q_out, lqo = _fresh_rows(q)
+        fresh.append(q_out)
+    else:
+        lqo = _bf16_rows(q_out, "q_out", q.shape)
     if k_out is None:
-        k_out = fresh_k = k.new_empty(k.shape)
+        k_out, lko = _fresh_rows(k)
+        fresh.append(k_out)
+    else:
+        lko = _bf16_rows(k_out, "k_out", k.shape)
     st = _lib.gqa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), B, T, Hq, Hkv, D, lq, lk,
-                               _bf16_rows(q_out, "q_out", q.shape), _bf16_rows(k_out, "k_out", k.shape), r,
-                               _stream_on(stream, device))
+                               lqo, lko, r, _stream_on(stream, device))
     if st != GQA_OK:
         raise GqaError(st, "gqa_qk_norm_rope")
     if stream is not None:
-        _keep_until(stream, fresh_q, fresh_k)
+        _keep_until(stream, *fresh)
     return q_out, k_out
 
 
@@ -1010,9 +1024,15 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, *, q_weight=None, k_weight=None, eps=
                         k_weight, cos, sin, positions)
     fresh = []
     if dq is None:
-        fresh.append(dq := q.new_empty(q.shape))
+        dq, ldq = _fresh_rows(q)
+        fresh.append(dq)
+    else:
+        ldq = _bf16_rows(dq, "dq", q.shape)
     if dk is None:
-        fresh.append(dk := k.new_empty(k.shape))
+        dk, ldk = _fresh_rows(k)
+        fresh.append(dk)
+    else:
+        ldk = _bf16_rows(dk, "dk", k.shape)
     dqw = dkw = None
     need = 0
     if q_weight is not None or k_weight is not None:
@@ -1034,7 +1054,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, *, q_weight=None, k_weight=None, eps=
     st = _lib.gqa_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
                                    dk.data_ptr(), _ptr(dqw), _ptr(dkw), B, T, Hq, Hkv, D,
                                    _bf16_rows(dq_out, "dq_out", q.shape), _bf16_rows(dk_out, "dk_out", k.shape), lq, lk,
-                                   _bf16_rows(dq, "dq", q.shape), _bf16_rows(dk, "dk", k.shape), r, ws_ptr, ws_bytes,
+                                   ldq, ldk, r, ws_ptr, ws_bytes,
                                    _stream_on(stream, device))
     if st != GQA_OK:
         raise GqaError(st, "gqa_qk_norm_rope_bwd")
@@ -1076,10 +1096,13 @@ def qk_norm_rope_append(q, k, v, k_pool, v_pool, slots, *, q_weight=None, k_weig
                         k_weight, cos, sin, positions)
     fresh = None
     if q_out is None:
-        q_out = fresh = q.new_empty(q.shape)
+        q_out, lqo = _fresh_rows(q)
+        fresh = q_out
+    else:
+        lqo = _bf16_rows(q_out, "q_out", q.shape, dims=3)
     st = _lib.gqa_qk_norm_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_pool.data_ptr(),
                                       v_pool.data_ptr(), slots.data_ptr(), N, Hq, Hkv, D, page, pages, lq, lk, lv,
-                                      _bf16_rows(q_out, "q_out", q.shape, dims=3), sk, sv, r, _stream_on(stream, device))
+                                      lqo, sk, sv, r, _stream_on(stream, device))
     if st != GQA_OK:
         raise GqaError(st, "gqa_qk_norm_rope_append")
     if stream is not None:
@@ -1138,7 +1161,7 @@ def kv4_gather(k_pool, v_pool, slots, *, k=None, v=None, stream=None):
     fresh = None
     if k is None and v is None:
         fresh = _Torch.empty((2, N, Hkv, D), dtype=_Torch.bf16, device=k_pool.device)
-        k, v = fresh.unbind(0)
+        k, v = fresh[0], fresh[1]
     elif k is None or v is None:
         fresh = _Torch.empty((N, Hkv, D), dtype=_Torch.bf16, device=k_pool.device)
         k, v = (fresh, v) if k is None else (k, fresh)
@@ -1178,7 +1201,7 @@ def attn_decode_kv4(q, k_pool, v_pool, seqlens_k, block_table, *, max_seqlen_k=N
                         workspace)
     fresh_out = fresh_ws = None
     if out is None:
-        out = fresh_out = q.new_empty(q.shape)
+        out = fresh_out = _Torch.empty_like(q)
     elif out.dtype is not _Torch.bf16 or out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 tensor shaped like q")
     if workspace is None:
