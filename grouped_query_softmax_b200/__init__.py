@@ -8,6 +8,12 @@ pointers as integers, sizes, strides, a stream handle). ``attn_fwd`` and
 layout, allocate the outputs (and the decode workspace) with torch, and call the
 same entry points. PyTorch supplies device memory and streams only.
 
+Around the attention calls, for torch tensors in the same way: ``paged_plan`` (block
+tables and cache rows of a step, on the device), ``qk_norm_rope`` with its backward and
+its cache-writing form, and a paged cache held in 4 bits (``kv4_append``,
+``kv4_gather``, ``attn_decode_kv4``). These check that all operands are on the current
+device; a ``stream`` other than the current one has to be ordered after it by the caller.
+
 There is no CPU fallback: importing this package fails loudly if the CUDA
 library has not been built.
 """
