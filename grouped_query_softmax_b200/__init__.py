@@ -11,8 +11,9 @@ same entry points. PyTorch supplies device memory and streams only.
 Around the attention calls, for torch tensors in the same way: ``paged_plan`` (block
 tables and cache rows of a step, on the device), ``qk_norm_rope`` with its backward and
 its cache-writing form, and a paged cache held in 4 bits (``kv4_append``,
-``kv4_gather``, ``attn_decode_kv4``). These check that all operands are on the current
-device; a ``stream`` other than the current one has to be ordered after it by the caller.
+``kv4_gather``, ``attn_decode_kv4``). Their checks and allocations are in C++
+(``_torch_calls.so``, built with the library), since these calls take microseconds on the
+device. All operands must be on the current device; a ``stream`` other than the current one has to be ordered after it by the caller.
 
 There is no CPU fallback: importing this package fails loudly if the CUDA
 library has not been built.
@@ -20,7 +21,6 @@ library has not been built.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import NamedTuple
 
@@ -783,93 +783,39 @@ def _attn_fwd_varlen_paged(q, k_pool, v_pool, cu_seqlens_q, seqlens_q, seqlens_k
 
 
 # ---------------------------------------------------------------- around the attention calls
-class _Torch:
-    """torch's names that the calls below need, looked up on the first of them."""
-    tensor = None
-
-    @classmethod
-    def load(cls):
-        torch = _torch()
-        cls.bf16, cls.f32, cls.i32, cls.u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-        cls.empty, cls.empty_like, cls.rows = torch.empty, torch.empty_like, torch.contiguous_format
-        cls.current_device = torch.cuda.current_device
-        # the current stream without a Stream object
-        cls.stream = staticmethod(getattr(torch._C, "_cuda_getCurrentRawStream", None)
-                                  or (lambda device: torch.cuda.current_stream(device).cuda_stream))
-        cls.tensor = torch.Tensor
-        return cls.tensor
+_calls = None  # _torch_calls: checks, allocation and the C calls of the functions below
 
 
-def _on_device(names, *tensors):
-    """The index of the CUDA device that all given tensors (None: left out) are on; it must be the
-    current one."""
-    device = -2
-    for i, t in enumerate(tensors):
-        if t is None:
-            continue
-        d = t.get_device()
-        if d != device:
-            if d < 0:
-                raise TypeError(f"{names.split()[i]} must be a CUDA tensor")
-            if device != -2:
-                raise ValueError(f"{names.split()[i]} is on cuda:{d}, the first operand on cuda:{device}")
-            device = d
-    if device != _Torch.current_device():
-        raise ValueError(f"the operands are on cuda:{device}, which is not the current device")
-    return device
+def _load_calls():
+    """Load _torch_calls.so and give it the C entry points' addresses."""
+    global _calls
+    _torch()  # before the module, which needs its libraries
+    path = os.path.join(_HERE, "_torch_calls.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build the library first "
+                          "(python -c 'import __graft_entry__ as g; g.build()'). There is no fallback.")
+    from . import _torch_calls as calls
+    calls.set_functions(*[ctypes.cast(getattr(_lib, n), _vp).value for n in (
+        "gqa_paged_plan", "gqa_qk_norm_rope", "gqa_qk_norm_rope_append", "gqa_qk_norm_rope_bwd",
+        "gqa_qk_norm_rope_bwd_workspace_bytes", "gqa_kv4_append", "gqa_kv4_gather", "gqa_attn_decode_kv4",
+        "gqa_attn_decode_kv4_workspace_bytes")])
+    _calls = calls
+    return calls
+
+
+def _handle(stream):
+    return None if stream is None else _stream_handle(stream)
 
 
 def _keep_until(stream, *tensors):
-    """Tensors allocated here for a call on another stream than the current one stay allocated
-    until that stream has passed the call."""
+    """Tensors allocated for a call on another stream than the current one stay allocated until
+    that stream has passed the call."""
     torch = _torch()
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
-
-
-def _stream_on(stream, device):
-    return _Torch.stream(device) if stream is None else _stream_handle(stream)
-
-
-def _int32(t, name, shape=None):
-    if not isinstance(t, _Torch.tensor or _Torch.load()) or t.dtype is not _Torch.i32 or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous int32 tensor")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    return t
-
-
-@functools.lru_cache(maxsize=4096)
-def _c_layout(sb, sh, st):
-    return GqaLayout(sb, sh, st)
-
-
-@functools.lru_cache(maxsize=4096)
-def _c_layout4(sb, sh):
-    return GqaKv4Layout(sb, sh)
-
-
-def _fresh_rows(like):
-    """A contiguous tensor like the given one, [B, H, T, D] or [T, H, D], and its layout."""
-    shape = like.shape
-    D = shape[-1]
-    lay = _c_layout(shape[1] * shape[2] * D, shape[2] * D, D) if len(shape) == 4 else _c_layout(0, D, shape[1] * D)
-    return _Torch.empty_like(like, memory_format=_Torch.rows), lay
-
-
-def _bf16_rows(t, name, shape=None, dims=4):
-    """Layout of a bf16 operand [B, H, T, D], or [T, H, D] when dims is 3."""
-    if not isinstance(t, _Torch.tensor or _Torch.load()) or t.dtype is not _Torch.bf16:
-        raise TypeError(f"{name} must be a bf16 tensor")
-    st = t.stride()
-    if len(st) != dims or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must have the shape {tuple(shape) if shape else f'of {dims} axes'}, not {tuple(t.shape)}")
-    if st[-1] != 1:
-        raise ValueError(f"{name}: the last (D) axis must be contiguous")
-    return _c_layout(st[0], st[1], st[2]) if dims == 4 else _c_layout(0, st[1], st[0])
 
 
 class PagedPlan(NamedTuple):
@@ -895,84 +841,15 @@ def paged_plan(seqlens, new_tokens, block_table, free_list, free_count, *, page_
     ``seqlens`` and ``free_count`` themselves. Lengths that do not fit, or too few pages, leave
     everything as it is and are reported by ``gqa_get_device_error``.
     """
-    S = seqlens.numel()
-    for t, n in ((seqlens, "seqlens"), (new_tokens, "new_tokens")):
-        _int32(t, n, (S,))
-    if keep is not None:
-        _int32(keep, "keep", (S,))
-    _int32(block_table, "block_table")
-    _int32(free_list, "free_list")
-    if block_table.dim() != 2 or block_table.shape[0] != S or free_list.dim() != 1:
-        raise ValueError("block_table must be [S, max_pages] and free_list [capacity]")
-    if _int32(free_count, "free_count").numel() != 1:
-        raise ValueError("free_count must hold one value")
-    device = _on_device("seqlens new_tokens block_table free_list free_count keep", seqlens, new_tokens, block_table,
-                        free_list, free_count, keep)
-    max_tokens = int(max_tokens)
-    fresh = None
-    if out is None:
-        if max_tokens <= 0:
-            raise ValueError("max_tokens must be positive")
-        # one allocation; positions and slots start on 16 bytes
-        pad = -(max_tokens + 2 * S + 2) % 4
-        fresh = seqlens.new_empty(2 * max_tokens + 2 * S + 2 + pad)
-        if pad:
-            pos, lens, cu, count, _, slots = fresh.split_with_sizes((max_tokens, S, S + 1, 1, pad, max_tokens))
-        else:
-            pos, lens, cu, count, slots = fresh.split_with_sizes((max_tokens, S, S + 1, 1, max_tokens))
-        out = PagedPlan(lens, cu, pos, slots, count)
-    else:
-        for t, n, shape in zip(out, PagedPlan._fields, ((S,), (S + 1,), (max_tokens,), (max_tokens,), (1,))):
-            _int32(t, n, shape)
-        _on_device("seqlens " + " ".join(PagedPlan._fields), seqlens, *out)
-    st = _lib.gqa_paged_plan(seqlens.data_ptr(), _ptr(keep), new_tokens.data_ptr(), block_table.data_ptr(),
-                             free_list.data_ptr(), free_count.data_ptr(), out.seqlens_k.data_ptr(),
-                             out.cu_seqlens.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
-                             out.free_count.data_ptr(), S, block_table.shape[1], page_size, num_pages,
-                             free_list.numel(), max_tokens, _stream_on(stream, device))
-    if st != GQA_OK:
-        raise GqaError(st, "gqa_paged_plan")
+    r = (_calls or _load_calls()).paged_plan(seqlens, new_tokens, block_table, free_list, free_count, keep, out, page_size,
+                                             num_pages, max_tokens, _handle(stream))
+    if type(r) is int:
+        raise GqaError(r, "gqa_paged_plan")
+    if out is not None:
+        return out
     if stream is not None:
-        _keep_until(stream, fresh)
-    return out
-
-
-def _rope_args(D, B, T, q_weight, k_weight, eps, cos, sin, positions, interleaved):
-    """The GqaRope of a call."""
-    q_ptr = k_ptr = cos_ptr = sin_ptr = pos_ptr = None
-    fp32 = pos_sb = rows = rot = 0
-    if q_weight is not None:
-        q_ptr, fp32 = q_weight.data_ptr(), q_weight.dtype is _Torch.f32
-        if q_weight.shape != (D,) or not q_weight.is_contiguous() or not (fp32 or q_weight.dtype is _Torch.bf16):
-            raise TypeError(f"q_weight must be a contiguous bf16 or fp32 tensor [{D}]")
-    if k_weight is not None:
-        k_ptr, k_fp32 = k_weight.data_ptr(), k_weight.dtype is _Torch.f32
-        if k_weight.shape != (D,) or not k_weight.is_contiguous() or not (k_fp32 or k_weight.dtype is _Torch.bf16):
-            raise TypeError(f"k_weight must be a contiguous bf16 or fp32 tensor [{D}]")
-        if q_weight is not None and k_fp32 is not fp32:
-            raise TypeError("q_weight and k_weight must have the same type")
-        fp32 = k_fp32
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin come together")
-    if cos is not None:
-        shape = cos.shape
-        if (len(shape) != 2 or sin.shape != shape or cos.dtype is not _Torch.f32 or sin.dtype is not _Torch.f32
-                or not cos.is_contiguous() or not sin.is_contiguous()):
-            raise TypeError("cos and sin must be contiguous fp32 tensors [positions, rot / 2]")
-        cos_ptr, sin_ptr, rows, rot = cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1]
-        if positions is not None:
-            _int32(positions, "positions")
-            if positions.shape != (T,):
-                if positions.shape != (B, T):
-                    raise ValueError(f"positions must be [{T}] or [{B}, {T}]")
-                pos_sb = T
-            pos_ptr = positions.data_ptr()
-    elif positions is not None:
-        raise ValueError("positions need cos and sin")
-    return GqaRope(q_ptr, k_ptr, cos_ptr, sin_ptr, pos_ptr, pos_sb, rows, rot, bool(interleaved), fp32, eps)
-
-
-_ROPE_NAMES = " q_weight k_weight cos sin positions"
+        _keep_until(stream, *r)
+    return PagedPlan(*r)
 
 
 def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, eps=1e-6, cos=None, sin=None, positions=None,
@@ -986,32 +863,13 @@ def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, eps=1e-6, cos=None, sin=
     pairs are (i, i + rot/2), or (2i, 2i + 1) when ``interleaved``. Returns contiguous (q, k) of
     the same shapes, or writes ``q_out``/``k_out`` (which may be q and k themselves).
     """
-    lq = _bf16_rows(q, "q")
-    B, Hq, T, D = q.shape
-    lk = _bf16_rows(k, "k")
-    Hkv = k.shape[1]
-    if k.shape != (B, Hkv, T, D):
-        raise ValueError("q and k must be [B, Hq, T, D] and [B, Hkv, T, D]")
-    r = _rope_args(D, B, T, q_weight, k_weight, eps, cos, sin, positions, interleaved)
-    device = _on_device("q k q_out k_out" + _ROPE_NAMES, q, k, q_out, k_out, q_weight, k_weight, cos, sin, positions)
-    fresh = []
-    if q_out is None:
-        q_out, lqo = _fresh_rows(q)
-        fresh.append(q_out)
-    else:
-        lqo = _bf16_rows(q_out, "q_out", q.shape)
-    if k_out is None:
-        k_out, lko = _fresh_rows(k)
-        fresh.append(k_out)
-    else:
-        lko = _bf16_rows(k_out, "k_out", k.shape)
-    st = _lib.gqa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), B, T, Hq, Hkv, D, lq, lk,
-                               lqo, lko, r, _stream_on(stream, device))
-    if st != GQA_OK:
-        raise GqaError(st, "gqa_qk_norm_rope")
+    r = (_calls or _load_calls()).qk_norm_rope(q, k, q_weight, k_weight, eps, cos, sin, positions, interleaved, q_out, k_out,
+                                               _handle(stream))
+    if type(r) is int:
+        raise GqaError(r, "gqa_qk_norm_rope")
     if stream is not None:
-        _keep_until(stream, *fresh)
-    return q_out, k_out
+        _keep_until(stream, *(t for t, given in zip(r, (q_out, k_out)) if given is None))
+    return r
 
 
 def qk_norm_rope_bwd(dq_out, dk_out, q, k, *, q_weight=None, k_weight=None, eps=1e-6, cos=None, sin=None,
@@ -1019,54 +877,13 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, *, q_weight=None, k_weight=None, eps=
     """Gradients (dq, dk, dq_weight, dk_weight) of ``qk_norm_rope(q, k, ...)`` for the gradients of
     its outputs (for instance ``attn_bwd``'s dq and dk). The weights' gradients are fp32 [D], None
     for a side without a weight. dq and dk may be dq_out and dk_out themselves."""
-    lq = _bf16_rows(q, "q")
-    B, Hq, T, D = q.shape
-    lk = _bf16_rows(k, "k")
-    Hkv = k.shape[1]
-    if k.shape != (B, Hkv, T, D):
-        raise ValueError("q and k must be [B, Hq, T, D] and [B, Hkv, T, D]")
-    r = _rope_args(D, B, T, q_weight, k_weight, eps, cos, sin, positions, interleaved)
-    device = _on_device("dq_out dk_out q k dq dk workspace" + _ROPE_NAMES, dq_out, dk_out, q, k, dq, dk, workspace, q_weight,
-                        k_weight, cos, sin, positions)
-    fresh = []
-    if dq is None:
-        dq, ldq = _fresh_rows(q)
-        fresh.append(dq)
-    else:
-        ldq = _bf16_rows(dq, "dq", q.shape)
-    if dk is None:
-        dk, ldk = _fresh_rows(k)
-        fresh.append(dk)
-    else:
-        ldk = _bf16_rows(dk, "dk", k.shape)
-    dqw = dkw = None
-    need = 0
-    if q_weight is not None or k_weight is not None:
-        if workspace is None:
-            need = gqa_qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hkv, D)
-        # one allocation: the weights' gradients behind the workspace
-        buf = _Torch.empty(need // 4 + 2 * D, dtype=_Torch.f32, device=q.device)
-        fresh.append(buf)
-        ws_ptr, ws_bytes = buf.data_ptr(), need
-        if workspace is not None:
-            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        _, dqw, dkw = buf.split_with_sizes((need // 4, D, D))
-        if q_weight is None:
-            dqw = None
-        if k_weight is None:
-            dkw = None
-    else:
-        ws_ptr, ws_bytes = None, 0
-    st = _lib.gqa_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
-                                   dk.data_ptr(), _ptr(dqw), _ptr(dkw), B, T, Hq, Hkv, D,
-                                   _bf16_rows(dq_out, "dq_out", q.shape), _bf16_rows(dk_out, "dk_out", k.shape), lq, lk,
-                                   ldq, ldk, r, ws_ptr, ws_bytes,
-                                   _stream_on(stream, device))
-    if st != GQA_OK:
-        raise GqaError(st, "gqa_qk_norm_rope_bwd")
-    if stream is not None:
-        _keep_until(stream, *fresh)
-    return dq, dk, dqw, dkw
+    r = (_calls or _load_calls()).qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, eps, cos, sin, positions,
+                                                   interleaved, dq, dk, workspace, _handle(stream))
+    if type(r) is int:
+        raise GqaError(r, "gqa_qk_norm_rope_bwd")
+    if stream is not None:  # a workspace made for the call lies in front of the weights' gradients
+        _keep_until(stream, *(t for t, given in zip(r, (dq, dk, None, None)) if given is None))
+    return r
 
 
 def qk_norm_rope_append(q, k, v, k_pool, v_pool, slots, *, q_weight=None, k_weight=None, eps=1e-6, cos=None, sin=None,
@@ -1078,42 +895,15 @@ def qk_norm_rope_append(q, k, v, k_pool, v_pool, slots, *, q_weight=None, k_weig
     pools of ``attn_decode_varlen``, [pages, page, Hkv, D] ("NHD") or [pages, Hkv, page, D] ("HND").
     Returns the queries [N, Hq, D].
     """
-    lq = _bf16_rows(q, "q", dims=3)
-    N, Hq, D = q.shape
-    lk = _bf16_rows(k, "k", dims=3)
-    Hkv = k.shape[1]
-    lv = _bf16_rows(v, "v", (N, Hkv, D), dims=3)
-    if k.shape != (N, Hkv, D):
-        raise ValueError("q and k must be [N, Hq, D] and [N, Hkv, D]")
-    _int32(slots, "slots", (N,))
-    sk = _bf16_rows(k_pool, "k_pool")
-    sv = _bf16_rows(v_pool, "v_pool", k_pool.shape)
-    if pool_layout == "NHD":
-        pages, page, heads, _ = k_pool.shape
-        sk, sv = _c_layout(sk.sb, sk.st, sk.sh), _c_layout(sv.sb, sv.st, sv.sh)
-    elif pool_layout == "HND":
-        pages, heads, page, _ = k_pool.shape
-    else:
+    if pool_layout not in ("NHD", "HND"):
         raise ValueError("pool_layout must be 'NHD' or 'HND'")
-    if heads != Hkv or k_pool.shape[3] != D:
-        raise ValueError("the pools' heads and rows must be k's")
-    r = _rope_args(D, 1, N, q_weight, k_weight, eps, cos, sin, positions, interleaved)
-    device = _on_device("q k v k_pool v_pool slots q_out" + _ROPE_NAMES, q, k, v, k_pool, v_pool, slots, q_out, q_weight,
-                        k_weight, cos, sin, positions)
-    fresh = None
-    if q_out is None:
-        q_out, lqo = _fresh_rows(q)
-        fresh = q_out
-    else:
-        lqo = _bf16_rows(q_out, "q_out", q.shape, dims=3)
-    st = _lib.gqa_qk_norm_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_pool.data_ptr(),
-                                      v_pool.data_ptr(), slots.data_ptr(), N, Hq, Hkv, D, page, pages, lq, lk, lv,
-                                      lqo, sk, sv, r, _stream_on(stream, device))
-    if st != GQA_OK:
-        raise GqaError(st, "gqa_qk_norm_rope_append")
-    if stream is not None:
-        _keep_until(stream, fresh)
-    return q_out
+    r = (_calls or _load_calls()).qk_norm_rope_append(q, k, v, k_pool, v_pool, slots, q_weight, k_weight, eps, cos, sin,
+                                                      positions, interleaved, pool_layout == "NHD", q_out, _handle(stream))
+    if type(r) is int:
+        raise GqaError(r, "gqa_qk_norm_rope_append")
+    if stream is not None and q_out is None:
+        _keep_until(stream, r)
+    return r
 
 
 def kv4_pool(num_pages, num_heads, page_size, D, device=None):
@@ -1123,32 +913,10 @@ def kv4_pool(num_pages, num_heads, page_size, D, device=None):
                        device=torch.cuda.current_device() if device is None else device)
 
 
-def _kv4_layout(t, name, D, shape=None):
-    """Layout of a 4-bit pool [pages, Hkv, page, D / 2 + 4]."""
-    if not isinstance(t, _Torch.tensor or _Torch.load()) or t.dtype is not _Torch.u8:
-        raise TypeError(f"{name} must be a uint8 tensor")
-    if t.dim() != 4 or t.shape[3] != D // 2 + 4 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must be [pages, Hkv, page, {D // 2 + 4}] (both pools alike), not {tuple(t.shape)}")
-    st = t.stride()
-    if st[3] != 1 or st[2] != t.shape[3]:
-        raise ValueError(f"{name}: the rows of a page must be packed")
-    return _c_layout4(st[0], st[1])
-
-
 def kv4_append(k, v, k_pool, v_pool, slots, *, stream=None):
     """Write k and v, bf16 [N, Hkv, D] (any token/head strides), as 4-bit rows to the rows
     ``slots`` (int32 [N], distinct; negative: none) of the pools [pages, Hkv, page, D / 2 + 4]."""
-    lk = _bf16_rows(k, "k", dims=3)
-    N, Hkv, D = k.shape
-    lv = _bf16_rows(v, "v", k.shape, dims=3)
-    _int32(slots, "slots", (N,))
-    sk = _kv4_layout(k_pool, "k_pool", D)
-    sv = _kv4_layout(v_pool, "v_pool", D, k_pool.shape)
-    if k_pool.shape[1] != Hkv:
-        raise ValueError("the pools' heads must be k's")
-    device = _on_device("k v k_pool v_pool slots", k, v, k_pool, v_pool, slots)
-    st = _lib.gqa_kv4_append(k.data_ptr(), v.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), slots.data_ptr(), N, Hkv, D,
-                             k_pool.shape[2], k_pool.shape[0], lk, lv, sk, sv, _stream_on(stream, device))
+    st = (_calls or _load_calls()).kv4_append(k, v, k_pool, v_pool, slots, _handle(stream))
     if st != GQA_OK:
         raise GqaError(st, "gqa_kv4_append")
 
@@ -1156,29 +924,12 @@ def kv4_append(k, v, k_pool, v_pool, slots, *, stream=None):
 def kv4_gather(k_pool, v_pool, slots, *, k=None, v=None, stream=None):
     """Rows ``slots`` (int32 [N]) of the 4-bit pools as bf16 (k, v) [N, Hkv, D]; a slot outside
     the pool gives zeros."""
-    if not isinstance(k_pool, _Torch.tensor or _Torch.load()) or k_pool.dim() != 4:
-        raise TypeError("k_pool must be a uint8 tensor [pages, Hkv, page, D / 2 + 4]")
-    pages, Hkv, page, row = k_pool.shape
-    D = 2 * (row - 4)
-    sk = _kv4_layout(k_pool, "k_pool", D)
-    sv = _kv4_layout(v_pool, "v_pool", D, k_pool.shape)
-    N = _int32(slots, "slots").numel()
-    device = _on_device("k_pool v_pool slots k v", k_pool, v_pool, slots, k, v)
-    fresh = None
-    if k is None and v is None:
-        fresh = _Torch.empty((2, N, Hkv, D), dtype=_Torch.bf16, device=k_pool.device)
-        k, v = fresh[0], fresh[1]
-    elif k is None or v is None:
-        fresh = _Torch.empty((N, Hkv, D), dtype=_Torch.bf16, device=k_pool.device)
-        k, v = (fresh, v) if k is None else (k, fresh)
-    st = _lib.gqa_kv4_gather(k_pool.data_ptr(), v_pool.data_ptr(), k.data_ptr(), v.data_ptr(), slots.data_ptr(), N, Hkv, D,
-                             page, pages, sk, sv, _bf16_rows(k, "k", (N, Hkv, D), dims=3),
-                             _bf16_rows(v, "v", (N, Hkv, D), dims=3), _stream_on(stream, device))
-    if st != GQA_OK:
-        raise GqaError(st, "gqa_kv4_gather")
+    r = (_calls or _load_calls()).kv4_gather(k_pool, v_pool, slots, k, v, _handle(stream))
+    if type(r) is int:
+        raise GqaError(r, "gqa_kv4_gather")
     if stream is not None:
-        _keep_until(stream, fresh)
-    return k, v
+        _keep_until(stream, *(t for t, given in zip(r, (k, v)) if given is None))
+    return r
 
 
 def attn_decode_kv4(q, k_pool, v_pool, seqlens_k, block_table, *, max_seqlen_k=None, scale=None, window=0, out=None,
@@ -1190,37 +941,10 @@ def attn_decode_kv4(q, k_pool, v_pool, seqlens_k, block_table, *, max_seqlen_k=N
     [B, max_pages]. ``workspace``: a uint8 CUDA tensor of gqa_attn_decode_kv4_workspace_bytes(...)
     bytes, allocated here when omitted.
     """
-    if not isinstance(q, _Torch.tensor or _Torch.load()) or q.dtype is not _Torch.bf16 or not q.is_contiguous() or q.dim() not in (3, 4):
-        raise TypeError("q must be a contiguous bf16 tensor [B, Hq, Tq, D] or [B, Hq, D]")
-    B, Hq, D = q.shape[0], q.shape[1], q.shape[-1]
-    Tq = q.shape[2] if q.dim() == 4 else 1
-    sk = _kv4_layout(k_pool, "k_pool", D)
-    sv = _kv4_layout(v_pool, "v_pool", D, k_pool.shape)
-    pages, Hkv, page, _ = k_pool.shape
-    _int32(seqlens_k, "seqlens_k", (B,))
-    _int32(block_table, "block_table")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [B, max_pages]")
-    max_pages = block_table.shape[1]
-    max_seqlen_k = max_pages * page if max_seqlen_k is None else int(max_seqlen_k)
-    device = _on_device("q k_pool v_pool seqlens_k block_table out workspace", q, k_pool, v_pool, seqlens_k, block_table, out,
-                        workspace)
-    fresh_out = fresh_ws = None
-    if out is None:
-        out = fresh_out = _Torch.empty_like(q)
-    elif out.dtype is not _Torch.bf16 or out.shape != q.shape or not out.is_contiguous():
-        raise ValueError("out must be a contiguous bf16 tensor shaped like q")
-    if workspace is None:
-        need = _lib.gqa_attn_decode_kv4_workspace_bytes(B, Hq, Hkv, Tq, max_seqlen_k, D, window)
-        if need:
-            workspace = fresh_ws = _Torch.empty(need, dtype=_Torch.u8, device=q.device)
-    st = _lib.gqa_attn_decode_kv4(q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), out.data_ptr(), seqlens_k.data_ptr(),
-                                  block_table.data_ptr(), page, pages, max_pages, B, Hq, Hkv, Tq, max_seqlen_k, D, sk, sv,
-                                  float(scale or 0.0), window, _ptr(workspace),
-                                  workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                                  _stream_on(stream, device))
-    if st != GQA_OK:
-        raise GqaError(st, "gqa_attn_decode_kv4")
+    r = (_calls or _load_calls()).attn_decode_kv4(q, k_pool, v_pool, seqlens_k, block_table, max_seqlen_k, scale or 0.0, window,
+                                                  out, workspace, _handle(stream))
+    if type(r) is int:
+        raise GqaError(r, "gqa_attn_decode_kv4")
     if stream is not None:
-        _keep_until(stream, fresh_out, fresh_ws)
-    return out
+        _keep_until(stream, None if out is not None else r[0], None if workspace is not None else r[1])
+    return r[0]

@@ -1,9 +1,12 @@
-"""Build libgqa.so in-tree with nvcc for sm_100a (no JIT cache, no pip install)."""
+"""Build libgqa.so in-tree with nvcc for sm_100a, and _torch_calls.so, the torch side of the calls
+around the paged cache, with g++ against the installed torch (no JIT cache, no pip install)."""
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,12 +24,37 @@ FLAGS = [
 ]
 
 
+CALLS = os.path.join(HERE, "_torch_calls.so")
+CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
+
+
+def _calls_command(out):
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]  # torch itself is not imported
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    paths = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+             os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-o", out, CALLS_SOURCE,
+            *[x for d in paths for x in ("-isystem", d)], "-L" + os.path.join(torch, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
+
+
+def _calls_stale():
+    if not os.path.exists(CALLS):
+        return True
+    t = os.path.getmtime(CALLS)
+    return any(os.path.getmtime(p) > t for p in (CALLS_SOURCE, os.path.join(ROOT, "include", "gqa.h")))
+
+
 def _inputs():
     return ([os.path.join(CSRC, s) for s in SOURCES] + glob.glob(os.path.join(CSRC, "*.cuh"))
             + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 
 def stale() -> bool:
+    return _lib_stale() or _calls_stale()
+
+
+def _lib_stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
@@ -34,15 +62,19 @@ def stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile the CUDA library; returns its path. Raises CalledProcessError on failure."""
-    if not force and not stale():
-        return LIB
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [NVCC, *FLAGS, *extra_flags, "-o", tmp, *[os.path.join(CSRC, s) for s in SOURCES]]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.check_call(cmd)
-    os.replace(tmp, LIB)
+    """Compile the CUDA library and the torch side; returns the library's path. Raises
+    CalledProcessError on failure."""
+    for path, old, command in (
+            (LIB, _lib_stale, lambda tmp: [NVCC, *FLAGS, *extra_flags, "-o", tmp, *[os.path.join(CSRC, s) for s in SOURCES]]),
+            (CALLS, _calls_stale, _calls_command)):
+        if not force and not old():
+            continue
+        tmp = path + ".tmp%d" % os.getpid()
+        cmd = command(tmp)
+        if verbose:
+            print(" ".join(cmd))
+        subprocess.check_call(cmd)
+        os.replace(tmp, path)
     return LIB
 
 
