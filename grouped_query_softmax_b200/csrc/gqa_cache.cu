@@ -66,7 +66,8 @@ gqa_status paged_plan(const gqa::PagedPlanParams& p, cudaStream_t stream) {
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)gqa::paged_plan_smem(gqa::kPagedMaxSeqs)) != cudaSuccess)
         return GQA_ERR_CUDA;
-    const long long work = std::max<long long>(((long long)p.max_tokens + 3) / 4, p.S);  // four tokens a thread
+    // four tokens a thread, and one page that the step may take or give back
+    const long long work = ((long long)p.max_tokens + 3) / 4 + p.max_tokens / p.page_size + p.S;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = attr.val.clusterDim.y = attr.val.clusterDim.z = 1;

@@ -183,8 +183,10 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_paged_plan_kernel(const __gri
         p.cu[s] = cu[s];
         p.after[s] = keep_s[s] + (cu[s + 1] - cu[s]);
     }
-    for (int i = tid; i < n_push; i += threads) p.free_list[count + i] = released(i);
-    for (int j = tid; j < n_take; j += threads) {
+    // pages from the last thread down, tokens from the first up: where there are threads for both, they
+    // do not wait for one another
+    for (int i = threads - 1 - tid; i < n_push; i += threads) p.free_list[count + i] = released(i);
+    for (int j = threads - 1 - tid; j < n_take; j += threads) {
         const int s = paged_find(first_take, 0, p.S, j);
         p.table[(size_t)s * p.max_pages + had_s[s] + (j - first_take[s])] = taken(j);
     }
