@@ -129,11 +129,21 @@ __device__ __forceinline__ uint32_t dec4_halves(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Exponent field e of |x| for scaling x to [2^14, 2^15) by 2^(141 - e), whose own field is 268 - e,
-// and products with the codes back by 2^24 times the inverse, field e + 10; kept where both are
-// normal numbers (|x| from 2^-112 to 2^118).
-__device__ __forceinline__ int dec4_exponent(float x) { return min(max((int)(__float_as_uint(x) >> 23), 15), 244); }
+// Exponent field e of |x| for scaling x to [2^kTo, 2^(kTo + 1)), by dec4_up, and for taking products
+// with the codes back, by dec4_down (2^24 times the inverse); kept where both are normal numbers
+// (|x| from 2^-112 to 2^113).
+__device__ __forceinline__ int dec4_exponent(float x) { return min(max((int)(__float_as_uint(x) >> 23), 15), 240); }
 __device__ __forceinline__ float dec4_pow2(int field) { return __uint_as_float((uint32_t)field << 23); }
+template <int kTo>
+__device__ __forceinline__ float dec4_up(int e) { return dec4_pow2(254 + kTo - e); }
+template <int kTo>
+__device__ __forceinline__ float dec4_down(int e) { return dec4_pow2(e + 24 - kTo); }
+// The running maximum of a row's scores (log2 units) is raised once they pass it by more than kD4Slack:
+// a probability is then below 2^kD4Slack, and few tiles have to rescale what they add to (of 16
+// rows, one nearly always has a new maximum). w = p * step stays below 2^15.
+constexpr float kD4Slack = 4.f;
+constexpr int kD4StepTo = 10;  // the largest step yet is scaled to [2^10, 2^11)
+constexpr float kD4Lowest = -3.402823466e38f;  // the maximum of no scores
 
 // D = A(16x16 fp16, row) * B(16x8 fp16, col) + C, fp32 accumulate.
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -353,7 +363,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int ex = dec4_exponent(top);
-            const float up = dec4_pow2(268 - ex);
+            const float up = dec4_up<14>(ex);
 #pragma unroll
             for (int i = 0; i < kKI; ++i) {
 #pragma unroll
@@ -373,17 +383,18 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 sumq[nt][x] = __shfl_sync(0xffffffffu, sum, 8 * t + 4 * x) * 0x1p-24f;
-                unit[nt][x] = __shfl_sync(0xffffffffu, dec4_pow2(ex + 10), 8 * t + 4 * x) * p.scale_log2;
+                unit[nt][x] = __shfl_sync(0xffffffffu, dec4_down<14>(ex), 8 * t + 4 * x) * p.scale_log2;
             }
         }
         if constexpr (NT > 1) __syncwarp();
 
         float m[NT][2], l[NT][2], beta[NT][2];
         float oacc[kMT][NT][4], eights[NT][4];
-        float top_step = 0.f, up_step = dec4_pow2(268 - dec4_exponent(0.f));  // largest step yet, and w's factor
+        int step_ex = dec4_exponent(0.f);  // of the largest step yet
+        float up_step = dec4_up<kD4StepTo>(step_ex), step_limit = dec4_pow2(step_ex + 1);  // w's factor; the next exponent
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            m[nt][0] = m[nt][1] = -INFINITY;
+            m[nt][0] = m[nt][1] = kD4Lowest;
             l[nt][0] = l[nt][1] = beta[nt][0] = beta[nt][1] = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -495,37 +506,35 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                     vmid[j][c] = fmaf(8.f, vstep[j][c], dec4_least(head));
                     top = fmaxf(top, fabsf(vstep[j][c]));
                 }
-            bool raise = top > top_step;
-            float m_new[NT][2];
+            bool raise = top >= step_limit;
+            float mx[NT][2];  // of this lane's keys
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    float mx = -INFINITY;
+                    mx[nt][x] = -INFINITY;
 #pragma unroll
                     for (int j = 0; j < U; ++j)
 #pragma unroll
-                        for (int c = 0; c < 4; c += 2) mx = max3f(mx, score(j, c, nt, x), score(j, c + 1, nt, x));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    m_new[nt][x] = fmaxf(mx * unit[nt][x], m[nt][x]);
-                    raise |= m_new[nt][x] > m[nt][x];
+                        for (int c = 0; c < 4; c += 2) mx[nt][x] = max3f(mx[nt][x], score(j, c, nt, x), score(j, c + 1, nt, x));
+                    raise |= mx[nt][x] * unit[nt][x] > m[nt][x] + kD4Slack;
                 }
             if (__any_sync(0xffffffffu, raise)) {
-                // w = p * step is scaled so that the largest step yet is in [2^14, 2^15)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                top_step = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)), top_step);
-                const int ex = dec4_exponent(top_step);
-                const float down = dec4_pow2(268 - ex) / up_step;  // a power of two, or 0 past fp32's range
-                up_step = dec4_pow2(268 - ex);
+                step_ex = max(step_ex, dec4_exponent(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16))));
+                const float down = dec4_up<kD4StepTo>(step_ex) / up_step;  // a power of two, or 0 past fp32's range
+                up_step = dec4_up<kD4StepTo>(step_ex);
+                step_limit = step_ex < 240 ? dec4_pow2(step_ex + 1) : INFINITY;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float alpha = m_new[nt][x] > m[nt][x] ? ex2_approx(m[nt][x] - m_new[nt][x]) : 1.f;
-                        m[nt][x] = m_new[nt][x];
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx[nt][x] = fmaxf(mx[nt][x], __shfl_xor_sync(0xffffffffu, mx[nt][x], d));
+                        const float m_new = fmaxf(mx[nt][x] * unit[nt][x], m[nt][x]);
+                        const float alpha = ex2_approx(m[nt][x] - m_new);
+                        m[nt][x] = m_new;
                         l[nt][x] *= alpha;
                         beta[nt][x] *= alpha;
                         const float both = alpha * down;
@@ -537,11 +546,6 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                         }
                     }
             }
-            float neg_m[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) neg_m[nt][x] = m[nt][x] == -INFINITY ? 0.f : -m[nt][x];
             uint32_t pb[U][NT][4];  // B operand: keys 8t + c and 8t + 4 + c of query row g
             const auto weigh = [&](auto masked_keys) {
                 constexpr bool kMasked = decltype(masked_keys)::value;
@@ -555,7 +559,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
                                 const float sc = score(j, c, nt, x);
-                                const float e = ex2_approx(fmaf(sc, unit[nt][x], neg_m[nt][x]));
+                                const float e = ex2_approx(fmaf(sc, unit[nt][x], -m[nt][x]));
                                 l[nt][x] += e;
                                 if (kMasked && sc == -INFINITY) {  // such a key's step may be NaN
                                     w[x] = 0.f;
@@ -608,7 +612,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
 
         if constexpr (kCluster) {
             // ---- merge: the warp's state through its ring, the CTA's through its own place
-            const float down = dec4_pow2(dec4_exponent(top_step) + 10);  // 2^24 / up_step
+            const float down = dec4_down<kD4StepTo>(step_ex);
             const auto state = [&](uint8_t* base) { return reinterpret_cast<float*>(base); };  // m, l of each row, then O
             float* mine = state(ring);
 #pragma unroll
@@ -675,7 +679,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
             if (t0 == 0) e->x = (int)run;
             if (t1 == s.n) e->y = (int)run;
         }
-        const float down = dec4_pow2(dec4_exponent(top_step) + 10);  // 2^24 / up_step
+        const float down = dec4_down<kD4StepTo>(step_ex);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -551,8 +551,8 @@ GQA_API gqa_status gqa_kv4_gather(const void* k_pool, const void* v_pool, void* 
  * seqlens_k[b]; block_table int32 [B, max_pages] as there.
  *   Scores, softmax and sums are fp32, and the stored rows enter exactly. The product of a
  *   probability and a value row's step is rounded to fp16, relative to the largest step among
- *   the rows it is summed with: below 2^-28 of that it loses bits, below 2^-39 it vanishes.
- *   q and the steps are below 2^117 in size (or NaN, which stays with the queries that see it).
+ *   the rows it is summed with: below 2^-24 of that it loses bits, below 2^-35 it vanishes.
+ *   q and the steps are below 2^113 in size (or NaN, which stays with the queries that see it).
  *   Every L(b) must lie in [0, min(max_seqlen_k, max_pages * page_size)], max_seqlen_k <= 2^30.
  *   A query at a negative position (L(b) < Tq) sees no key and gets zeros. A sequence outside
  *   that range gets no output and is reported by the next gqa_get_device_error().
