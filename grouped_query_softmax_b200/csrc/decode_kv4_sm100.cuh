@@ -1,29 +1,40 @@
 // Decode over a paged cache held in 4 bits (rows as kv4_rows_sm100.cuh writes them): up to 16
 // new queries a sequence, any group size, optional sliding window.
 //
-// A stored row is k_j = s_j c_j + m_j with codes c in 0..15. With the offset z that unpacking adds
-// to a code,
-//   q . k_j = s_j (q . (z + c_j) - z . q) + m_j sum(q),
-//   sum_j p_j v_j = sum_j w_j (16 + c_j) - 24 sum_j w_j + sum_j p_j (m_j + 8 s_j),  w_j = bf16(p_j s_j):
-// the scales stay out of the products, which run on tensor cores with fp32 sums. K's products
-// are fp16 (codes and q fit it exactly, see below), V's bf16 (w needs the range). w is the only
-// rounding besides the output's: it is taken about the middle of the code range (8), so it
-// costs what rounding P to bf16 costs. A row's NaN can only reach the queries that see the key:
-// the codes themselves are always finite.
+// A stored row is k_j = s_j c_j + m_j with codes c in 0..15, so
+//   q . k_j = s_j (q . c_j) + m_j sum(q),
+//   sum_j p_j v_j = sum_j w_j (c_j - 8) + sum_j p_j (m_j + 8 s_j),   w_j = fp16(p_j s_j):
+// the scales stay out of the products, which run on tensor cores in fp16 with fp32 sums. A code
+// needs no conversion: its bits, masked out of the word, are the fp16 subnormal c * 2^-24 (16 c four
+// bits up), so eight codes cost four logic operations and one shift. q is exact in fp16 after a
+// scaling by a power of two a row (see below). w is the only rounding besides the output's; it is
+// scaled by the largest step seen, since a probability times a step can be of any size, and summed
+// about the middle of the code range (sum_j 8 w_j is one more product). A row's NaN can only reach
+// the queries that see the key: the codes themselves are always finite.
 //
 // Keys are the M dimension of the products and query rows their N (8 a tile), so that one
 // unpacked fragment serves every query row of the KV head. mma m16n8k16 takes any order of the
 // contracted index as long as both operands agree; the orders here are chosen so that every
 // fragment is whole 32-bit words of the packed rows: a row is D/8 + 1 words, which makes the
-// lanes' words (keys 4g + c, words t + 4i for K; keys 8t + c, words g + 8i for V) fall on 32
-// different banks without padding or swizzle. P goes from its accumulator layout to the B
-// operand's with one 8x8 transpose a tile.
+// lanes' words (keys 4g + c, words t + 4i) fall on 32 different banks without padding or swizzle.
+// Values and probabilities go to their operand layouts with 8x8 transposes (movmatrix, which leaves
+// the logic pipe alone). The unpacked operands are born in registers, which warp-level products
+// take as they are; tensor memory would take a store and a wait a tile more, and the tensor pipe is
+// at 30 %.
 //
-// Work: the tiles of every (sequence, KV head, row chunk) laid end to end are cut into equal runs,
-// one per warp, so all warps finish together whatever the lengths. A warp has a ring of its own
-// that its own lanes fill with bulk copies (a page's rows of one head are contiguous): no warp
-// waits for another. A unit cut between warps leaves fp32 partials that a second kernel merges
-// in a fixed order. Bound by HBM: D + 8 bytes a key and KV head.
+// Work, two forms. Few tiles: a cluster takes each (sequence, KV head, row chunk), its warps equal
+// parts of the tiles, and merges through shared memory: one launch (4099 keys, 8 KV heads of 4
+// queries, D = 128: 8.4 us; with runs and a merge 12.5). Many: the tiles of all units laid end
+// to end are cut into equal runs, one per warp, so all warps finish together whatever the lengths;
+// a unit cut between warps leaves fp32 partials that a second kernel merges in a fixed order. A warp
+// has a ring of its own that its own lanes fill with bulk copies (a page's rows of one head are
+// contiguous): no warp waits for another.
+//
+// The bytes are D + 8 a key and KV head; what bounds it is instructions. 64 sequences of 4096 to
+// 32768 keys, 8 KV heads of 4 queries, D = 128: 232 to 258 us, 5.1 to 5.7 TB/s, 78 to 87 % of the
+// measured copy rate, at 490 instructions a 32 keys, 57 % of the issue slots and 53 % of the
+// logic pipe (12 warps an SM; 16 with smaller rings were no faster). 64-key tiles where the
+// scores fit the registers: 32-key tiles took 8 % longer, by what is done once a tile.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -158,9 +169,7 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
     return d;
 }
 
-// kCluster: the form for few tiles, where a second launch would cost more than it balances. A
-// cluster takes each unit, its warps equal parts of the unit's tiles, and the states are merged
-// through shared memory: in the CTA, then over the cluster.
+// kCluster: the form for few tiles; the states are merged in the CTA, then over the cluster.
 template <int D, int NT, bool kCluster>
 __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCtasPerSm) gqa_decode_kv4_kernel(const Dec4Params p) {
     namespace cg = cooperative_groups;

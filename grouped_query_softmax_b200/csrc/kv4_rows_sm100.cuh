@@ -16,7 +16,8 @@
 // token, four rows at a time, and neighbouring teams neighbouring tokens, whose packed rows lie side
 // by side. The rows' extremes are exchanged together, each step halving the rows that a lane still
 // compares, and a row's step and its inverse are computed by a quarter of the lanes. Bound by
-// HBM: 2.53 bytes an element at D = 128.
+// HBM: 2.53 bytes an element at D = 128. 35197 tokens of 8 heads: written in 35 us and read back in
+// 30, 86 % of the measured copy rate together (140 us with a row a team).
 #pragma once
 
 #include "sm100_ptx.cuh"

