@@ -149,8 +149,8 @@ PyObject* tuple_of(std::initializer_list<at::Tensor> ts) {
 template <class F>
 PyObject* call(Py_ssize_t have, Py_ssize_t want, F f) {
     HANDLE_TH_ERRORS
-    if (have != want) type_error("expected " + std::to_string(want) + " arguments");
     try {
+        if (have != want) type_error("expected " + std::to_string(want) + " arguments");
         // outputs and their views are plain tensors: nothing here is differentiated by torch
         at::AutoDispatchBelowADInplaceOrView below_autograd;
         return f();
