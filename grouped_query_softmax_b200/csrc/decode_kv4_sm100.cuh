@@ -164,6 +164,23 @@ constexpr float kD4Slack = 4.f;
 constexpr int kD4StepTo = 10;  // the largest step yet is scaled to [2^10, 2^11)
 constexpr float kD4Lowest = -3.402823466e38f;  // the maximum of no scores
 
+// Two fp32 values in one instruction, denormals kept.
+__device__ __forceinline__ void dec4_fma2(float (&d)[2], const float (&a)[2], const float (&b)[2], const float (&c)[2]) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_pack(a[0], a[1])), "l"(f2_pack(b[0], b[1])), "l"(f2_pack(c[0], c[1])));
+    f2_unpack(r, d[0], d[1]);
+}
+__device__ __forceinline__ void dec4_mul2(float (&d)[2], const float (&a)[2], const float (&b)[2]) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_pack(a[0], a[1])), "l"(f2_pack(b[0], b[1])));
+    f2_unpack(r, d[0], d[1]);
+}
+__device__ __forceinline__ void dec4_add2(float (&d)[2], const float (&a)[2]) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_pack(d[0], d[1])), "l"(f2_pack(a[0], a[1])));
+    f2_unpack(r, d[0], d[1]);
+}
+
 // D = A(16x16 fp16, row) * B(16x8 fp16, col) + C, fp32 accumulate.
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                               uint32_t b1) {
@@ -405,13 +422,13 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
         }
         if constexpr (NT > 1) __syncwarp();
 
-        float m[NT][2], l[NT][2], beta[NT][2];
+        float less_m[NT][2], l[NT][2], beta[NT][2];
         float oacc[kMT][NT][4], eights[NT][4];
         int step_ex = dec4_exponent(0.f);  // of the largest step yet
         float up_step = dec4_up<kD4StepTo>(step_ex), step_limit = dec4_pow2(step_ex + 1);  // w's factor; the next exponent
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            m[nt][0] = m[nt][1] = kD4Lowest;
+            less_m[nt][0] = less_m[nt][1] = -kD4Lowest;
             l[nt][0] = l[nt][1] = beta[nt][0] = beta[nt][1] = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -487,10 +504,13 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                     const uint32_t head = K[(32 * j + 4 * g + c) * RW + D / 8];
                     const float step = dec4_step(head), least = dec4_least(head);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            score(j, c, nt, x) = fmaf(score(j, c, nt, x), step, least * sumq[nt][x]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float steps[2] = {step, step}, leasts[2] = {least, least};
+                        float sc[2] = {score(j, c, nt, 0), score(j, c, nt, 1)}, part[2];
+                        dec4_mul2(part, leasts, sumq[nt]);
+                        dec4_fma2(sc, sc, steps, part);
+                        score(j, c, nt, 0) = sc[0], score(j, c, nt, 1) = sc[1];
+                    }
                 }
             const bool masked = key0 + kKeys > pos_min + 1 || key0 < lo_max;
             if (masked) {
@@ -534,7 +554,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                     for (int j = 0; j < U; ++j)
 #pragma unroll
                         for (int c = 0; c < 4; c += 2) mx[nt][x] = max3f(mx[nt][x], score(j, c, nt, x), score(j, c + 1, nt, x));
-                    raise |= mx[nt][x] * unit[nt][x] > m[nt][x] + kD4Slack;
+                    raise |= fmaf(mx[nt][x], unit[nt][x], less_m[nt][x]) > kD4Slack;
                 }
             if (__any_sync(0xffffffffu, raise)) {
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
@@ -549,9 +569,9 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                     for (int x = 0; x < 2; ++x) {
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) mx[nt][x] = fmaxf(mx[nt][x], __shfl_xor_sync(0xffffffffu, mx[nt][x], d));
-                        const float m_new = fmaxf(mx[nt][x] * unit[nt][x], m[nt][x]);
-                        const float alpha = ex2_approx(m[nt][x] - m_new);
-                        m[nt][x] = m_new;
+                        const float m_new = fmaxf(mx[nt][x] * unit[nt][x], -less_m[nt][x]);
+                        const float alpha = ex2_approx(-less_m[nt][x] - m_new);
+                        less_m[nt][x] = -m_new;
                         l[nt][x] *= alpha;
                         beta[nt][x] *= alpha;
                         const float both = alpha * down;
@@ -572,18 +592,22 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            float w[2];
+                            const float sc[2] = {score(j, c, nt, 0), score(j, c, nt, 1)};
+                            float e[2], w[2];
+                            dec4_fma2(e, sc, unit[nt], less_m[nt]);
+                            e[0] = ex2_approx(e[0]);
+                            e[1] = ex2_approx(e[1]);
+                            dec4_add2(l[nt], e);
+const float vs = vstep[j][c] * up_step, vss[2] = {vs, vs}, mids[2] = {vmid[j][c], vmid[j][c]};
+                            if constexpr (kMasked) {  // such a key's step may be NaN
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const float sc = score(j, c, nt, x);
-                                const float e = ex2_approx(fmaf(sc, unit[nt][x], -m[nt][x]));
-                                l[nt][x] += e;
-                                if (kMasked && sc == -INFINITY) {  // such a key's step may be NaN
-                                    w[x] = 0.f;
-                                } else {
-                                    w[x] = e * (vstep[j][c] * up_step);
-                                    beta[nt][x] = fmaf(e, vmid[j][c], beta[nt][x]);
+                                for (int x = 0; x < 2; ++x) {
+                                    w[x] = sc[x] == -INFINITY ? 0.f : e[x] * vs;
+                                    if (sc[x] != -INFINITY) beta[nt][x] = fmaf(e[x], vmid[j][c], beta[nt][x]);
                                 }
+                            } else {
+                                dec4_mul2(w, e, vss);
+                                dec4_fma2(beta[nt], e, mids, beta[nt]);
                             }
                             pb[j][nt][c] = movmatrix_trans(dec4_halves(w[0], w[1]));
                         }
@@ -647,7 +671,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                         beta[nt][x] += __shfl_xor_sync(0xffffffffu, beta[nt][x], d);
                     }
                     const int n = 8 * nt + 2 * t + x;
-                    if (g == 0) mine[n] = m[nt][x], mine[C::kRows + n] = l[nt][x];
+                    if (g == 0) mine[n] = -less_m[nt][x], mine[C::kRows + n] = l[nt][x];
 #pragma unroll
                     for (int i = 0; i < kMT; ++i)
 #pragma unroll
@@ -715,7 +739,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                 if (n >= nrows) continue;
                 const float inv = l[nt][x] == 0.f ? 0.f : 1.f / l[nt][x];
                 if (!whole && g == 0)
-                    p.part_lse[part + n] = l[nt][x] == 0.f ? -INFINITY : m[nt][x] + __log2f(l[nt][x]);
+                    p.part_lse[part + n] = l[nt][x] == 0.f ? -INFINITY : __log2f(l[nt][x]) - less_m[nt][x];
 #pragma unroll
                 for (int i = 0; i < kMT / 4; ++i)
 #pragma unroll
