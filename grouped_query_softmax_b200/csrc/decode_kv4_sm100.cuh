@@ -6,7 +6,7 @@
 //   sum_j p_j v_j = sum_j w_j (c_j - 8) + sum_j p_j (m_j + 8 s_j),   w_j = fp16(p_j s_j):
 // the scales stay out of the products, which run on tensor cores in fp16 with fp32 sums. A code
 // needs no conversion: its bits, masked out of the word, are the fp16 subnormal c * 2^-24 (16 c four
-// bits up), so eight codes cost four logic operations and one shift (of values four operations). q is exact in fp16 after a
+// bits up), so eight codes cost four logic operations and one shift. q is exact in fp16 after a
 // scaling by a power of two a row (see below). w is the only rounding besides the output's; it is
 // scaled by the largest step seen, since a probability times a step can be of any size, and summed
 // about the middle of the code range (sum_j 8 w_j is one more product). A row's NaN can only reach
@@ -31,8 +31,8 @@
 // contiguous): no warp waits for another.
 //
 // The bytes are D + 8 a key and KV head; what bounds it is instructions. 64 sequences of 4096 to
-// 32768 keys, 8 KV heads of 4 queries, D = 128: 224 to 253 us, 5.3 to 5.9 TB/s, 80 to 90 % of the
-// measured copy rate, at 454 instructions a 32 keys, 56 % of the issue slots and 51 % of the
+// 32768 keys, 8 KV heads of 4 queries, D = 128: 232 to 258 us, 5.1 to 5.7 TB/s, 78 to 87 % of the
+// measured copy rate, at 490 instructions a 32 keys, 57 % of the issue slots and 53 % of the
 // logic pipe (12 warps an SM; 16 with smaller rings were no faster). 64-key tiles where the
 // scores fit the registers: 32-key tiles took 8 % longer, by what is done once a tile.
 #pragma once
@@ -132,14 +132,6 @@ __device__ __forceinline__ void dec4_codes(uint32_t w, uint32_t (&d)[4]) {
     d[1] = w & 0x00F000F0u;
     d[2] = up & 0x000F000Fu;
     d[3] = up & 0x00F000F0u;
-}
-// The same with one operation less: the last is of both codes of the byte, e = 2 at factor 1 and e = 3
-// at factor 16, for sums of which the other's can be taken away.
-__device__ __forceinline__ void dec4_codes_both(uint32_t w, uint32_t (&d)[4]) {
-    d[0] = w & 0x000F000Fu;
-    d[1] = w & 0x00F000F0u;
-    d[3] = __byte_perm(w, 0u, 0x4341);
-    d[2] = d[3] & 0x000F000Fu;
 }
 // The step and the minimum of a row from its last word.
 __device__ __forceinline__ float dec4_step(uint32_t head) { return __uint_as_float(head << 16); }
@@ -637,7 +629,7 @@ const float vs = vstep[j][c] * up_step, vss[2] = {vs, vs}, mids[2] = {vmid[j][c]
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int r = 0; r < 2; ++r)
-                            dec4_codes_both(movmatrix_trans(vr[(32 * (ks / 2) + c0 + c) * RW + 8 * i + 4 * r]), v[c][r]);
+                            dec4_codes(movmatrix_trans(vr[(32 * (ks / 2) + c0 + c) * RW + 8 * i + 4 * r]), v[c][r]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) product(oacc[4 * i + e], v[0][0][e], v[0][1][e], v[1][0][e], v[1][1][e]);
                 }
@@ -650,11 +642,6 @@ const float vs = vstep[j][c] * up_step, vss[2] = {vs, vs}, mids[2] = {vmid[j][c]
             }
         }
         if constexpr (NT > 1) __syncwarp();  // every lane has read the Q fragments
-        // Sum of w c: odd codes count 16 times, and tiles 4i + 3 hold those of tiles 4i + 2 too.
-        const auto code_sum = [&](int i, int nt, int e) {
-            const float o = i % 4 == 3 ? oacc[i][nt][e] - oacc[i - 1][nt][e] : oacc[i][nt][e];
-            return i % 2 ? o * 0.0625f : o;
-        };
 
         if constexpr (kCluster) {
             // ---- merge: the warp's state through its ring, the CTA's through its own place
@@ -676,7 +663,7 @@ const float vs = vstep[j][c] * up_step, vss[2] = {vs, vs}, mids[2] = {vmid[j][c]
                     for (int i = 0; i < kMT; ++i)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const float o = code_sum(i, nt, 2 * r + x);
+                            const float o = oacc[i][nt][2 * r + x] * (i % 2 ? 0.0625f : 1.f);  // odd codes count 16 times
                             mine[2 * C::kRows + n * D + 64 * (i / 4) + 32 * r + 4 * g + i % 4] =
                                 fmaf(o - eights[nt][x], down, beta[nt][x]);
                         }
@@ -747,7 +734,7 @@ const float vs = vstep[j][c] * up_step, vss[2] = {vs, vs}, mids[2] = {vmid[j][c]
                         float v[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float o = code_sum(4 * i + e, nt, 2 * r + x);
+                            const float o = oacc[4 * i + e][nt][2 * r + x] * (e % 2 ? 0.0625f : 1.f);  // odd codes count 16 times
                             v[e] = fmaf(o - eights[nt][x], down, beta[nt][x]) * inv;
                         }
                         const int d = 64 * i + 32 * r + 4 * g;
