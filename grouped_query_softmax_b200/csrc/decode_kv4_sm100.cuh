@@ -31,8 +31,8 @@
 // contiguous): no warp waits for another.
 //
 // The bytes are D + 8 a key and KV head; what bounds it is instructions. 64 sequences of 4096 to
-// 32768 keys, 8 KV heads of 4 queries, D = 128: 232 to 258 us, 5.1 to 5.7 TB/s, 78 to 87 % of the
-// measured copy rate, at 490 instructions a 32 keys, 57 % of the issue slots and 53 % of the
+// 32768 keys, 8 KV heads of 4 queries, D = 128: 225 to 255 us, 5.2 to 5.9 TB/s, 79 to 90 % of the
+// measured copy rate, at 449 instructions a 32 keys, 54 % of the issue slots and 55 % of the
 // logic pipe (12 warps an SM; 16 with smaller rings were no faster). 64-key tiles where the
 // scores fit the registers: 32-key tiles took 8 % longer, by what is done once a tile.
 #pragma once
