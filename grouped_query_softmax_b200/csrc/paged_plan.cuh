@@ -148,19 +148,22 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_paged_plan_kernel(const __gri
     bad = __syncthreads_or(bad);
     if constexpr (kCluster) cg::this_cluster().sync();  // every CTA has read the lengths and the count
 
-    const int threads = (int)gridDim.x * kThreads;
-    const int tid = (int)blockIdx.x * kThreads + threadIdx.x;
+    // Unsigned: max_tokens and free_capacity may be 2^31 - 1, and a thread steps past them by up to the grid's
+    // threads times four.
+    const unsigned threads = gridDim.x * kThreads;
+    const unsigned tid = blockIdx.x * kThreads + threadIdx.x;
+    const unsigned n_slots = p.max_tokens;
     if (bad) {  // nothing happens to the cache; the outputs describe an empty step
         if (tid == 0) {
             atomicOr(p.err, kDevErrBadSeqlens);
             p.cu[p.S] = 0;
             if (p.free_count_out != p.free_count) *p.free_count_out = count;
         }
-        for (int s = tid; s < p.S; s += threads) {
+        for (unsigned s = tid; s < (unsigned)p.S; s += threads) {
             p.cu[s] = 0;
             if (p.after != p.held) p.after[s] = p.held[s];
         }
-        for (int t = tid; t < p.max_tokens; t += threads) {
+        for (unsigned t = tid; t < n_slots; t += threads) {
             p.positions[t] = 0;
             p.slots[t] = -1;
         }
@@ -178,29 +181,29 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_paged_plan_kernel(const __gri
 
     if (tid == 0) {
         p.cu[p.S] = cu[p.S];
-        *p.free_count_out = count + n_give - n_take;
+        *p.free_count_out = count + (n_give - n_take);
     }
-    for (int s = tid; s < p.S; s += threads) {
+    for (unsigned s = tid; s < (unsigned)p.S; s += threads) {
         p.cu[s] = cu[s];
         p.after[s] = keep_s[s] + (cu[s + 1] - cu[s]);
     }
     // pages from the last thread down, tokens from the first up: where there are threads for both, they
     // do not wait for one another
-    for (int i = threads - 1 - tid; i < n_push; i += threads) p.free_list[count + i] = released(i);
-    for (int j = threads - 1 - tid; j < n_take; j += threads) {
-        const int s = paged_find(first_take, 0, p.S, j);
+    for (unsigned i = threads - 1 - tid; i < (unsigned)n_push; i += threads) p.free_list[count + i] = released((int)i);
+    for (unsigned i = threads - 1 - tid; i < (unsigned)n_take; i += threads) {
+        const int j = (int)i, s = paged_find(first_take, 0, p.S, j);
         p.table[(size_t)s * p.max_pages + had_s[s] + (j - first_take[s])] = taken(j);
     }
     // four tokens a thread, stored as one vector each; the last ones may be padding
     const int total = cu[p.S];
-    for (int t0 = tid * 4; t0 < p.max_tokens; t0 += threads * 4) {
+    for (unsigned t0 = tid * 4; t0 < n_slots; t0 += threads * 4) {
         int pos[4], slot[4];
         int s = 0, ordinal = -1, page = 0;
         for (int e = 0; e < 4; ++e) {
-            const int t = t0 + e;
             pos[e] = 0;
             slot[e] = -1;
-            if (t >= total) continue;
+            if (t0 + e >= (unsigned)total) continue;
+            const int t = (int)(t0 + e);
             if (e == 0 || t >= cu[s + 1]) {
                 s = paged_find(cu, s, p.S, t);
                 ordinal = -1;
@@ -217,11 +220,11 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_paged_plan_kernel(const __gri
             else
                 atomicOr(p.err, kDevErrBadSeqlens);
         }
-        if (t0 + 4 <= p.max_tokens) {
+        if (t0 + 4 <= n_slots) {
             *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
             *reinterpret_cast<int4*>(p.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
         } else {
-            for (int e = 0; t0 + e < p.max_tokens; ++e) {
+            for (int e = 0; t0 + e < n_slots; ++e) {
                 p.positions[t0 + e] = pos[e];
                 p.slots[t0 + e] = slot[e];
             }
