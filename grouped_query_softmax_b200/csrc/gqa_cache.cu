@@ -347,6 +347,7 @@ gqa_status gqa_paged_plan(const int* seqlens, const int* keep, const int* new_to
     gqa_status st = check_pages(page_size, num_pages);
     if (st != GQA_OK) return st;
     if (S > gqa::kPagedMaxSeqs || (long long)max_pages * page_size > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
+    if ((long long)S * max_pages > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;  // pages of a step are counted in 32 bits
     if (!aligned(seqlens, 4) || !aligned_or_null(keep, 4) || !aligned(new_tokens, 4) || !aligned(block_table, 4) ||
         !aligned(free_list, 4) || !aligned(free_count, 4) || !aligned(seqlens_out, 4) || !aligned(cu_seqlens, 4) ||
         !aligned(positions, 16) || !aligned(slots, 16) || !aligned(free_count_out, 4))

@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_paged_plan_kernel(const __gri
     const long long capacity = (long long)p.max_pages * p.page_size;
     const int count = *p.free_count;
     bool bad = false;
-    unsigned long long tokens = 0, pages = 0;  // running totals; pages: released << 32 | taken
+    // running totals; pages: released << 32 | taken, each at most S * max_pages < 2^31 (checked on the host)
+    unsigned long long tokens = 0, pages = 0;
     for (int base = 0; base < p.S; base += kThreads) {
         const int s = base + threadIdx.x;
         int held = 0, keep = 0, added = 0;

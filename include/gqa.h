@@ -418,8 +418,9 @@ GQA_API gqa_status gqa_attn_bwd(const void* q, const void* k, const void* v, con
  * order of (request, page), then the wanted ones are popped in that order, the last pushed page
  * first. The result does not depend on timing.
  *   seqlens, keep, new_tokens  int32 [S]; 0 <= keep <= seqlens; S <= 8192.
- *   block_table    int32 [S, max_pages]; entries below a request's page count are read, the
- *                  entries of the pages it takes are written, others keep what they hold.
+ *   block_table    int32 [S, max_pages], S * max_pages < 2^31; entries below a request's page
+ *                  count are read, the entries of the pages it takes are written, others keep
+ *                  what they hold.
  *   free_list      int32 [free_capacity]; entries at and past the new count keep what they hold.
  *   free_count     int32 [1]; free_count_out int32 [1], may be free_count itself.
  *   seqlens_out    int32 [S], may be seqlens, keep or new_tokens itself.

@@ -1,0 +1,18 @@
+"""What the operators around the paged cache refuse at the ends of their ranges, without a GPU."""
+import pytest
+
+
+@pytest.fixture(scope="module")
+def gqa():
+    import grouped_query_softmax_b200 as m
+    return m
+
+
+P = 1 << 20  # an aligned fake device address; never dereferenced on these paths
+
+
+@pytest.mark.parametrize("S,max_pages,page", [(8192, 1 << 18, 16), (8192, 1 << 20, 64), (128, 1 << 24, 16)])
+def test_plan_refuses_tables_of_more_pages_than_it_counts(gqa, S, max_pages, page):
+    """Every request may give all its pages back at once: their number has to fit 32 bits."""
+    st = gqa.gqa_paged_plan(P, P, P, P, P, P, 2 * P, 2 * P, 2 * P, 2 * P, 2 * P, S, max_pages, page, 1000, 1000, 64)
+    assert st == gqa.GQA_ERR_UNSUPPORTED
