@@ -64,6 +64,7 @@ struct Dec4Params {
     float* part;      // [2 * warps, rows, D] partial outputs
     float* part_lse;  // [2 * warps, rows] log2-domain log-sum-exp
     int2* ends;       // [B * Hkv * n_rc] first and last run of each unit's pieces
+    int runs;         // that the workspace has room for
     uint32_t* err;
     unsigned long long timeout_ns;
 };
@@ -748,7 +749,8 @@ const float vs = vstep[j][c] * up_step, vss[2] = {vs, vs}, mids[2] = {vmid[j][c]
 }
 
 // Merge the pieces of the units that were cut between warps, in run order: one block a row, of
-// sequence blockIdx.x. Which runs they are the first kernel has left.
+// sequence blockIdx.x. Which runs they are the first kernel has left; a warp of it whose wait ran
+// out has not, so `ends` may be anything the workspace held, and is only followed inside it.
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * kD4MergeWarps) gqa_decode_kv4_merge_kernel(const Dec4Params p) {
     constexpr int kRows = 8 * NT;
@@ -761,6 +763,7 @@ __global__ void __launch_bounds__(32 * kD4MergeWarps) gqa_decode_kv4_merge_kerne
     const int2 ends = p.ends[((size_t)blockIdx.x * p.Hkv + h) * p.n_rc + rc];
     const int len = __ldg(p.seqlens + blockIdx.x);
     if (len < 0 || len > p.capacity || ends.x == ends.y) return;  // no output, or whole
+    if (ends.x < 0 || ends.x > ends.y || ends.y >= p.runs) return;  // a wait ran out, which is reported
     const size_t row = (size_t)blockIdx.x * gridDim.y + blockIdx.y;
     const int c0 = ends.x, c1 = ends.y;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -7,8 +7,10 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/gqa.h"
+#include "../../include/gqa_testing.h"
 #include "decode_kv4_sm100.cuh"
 #include "gqa_internal.h"
 #include "kv4_rows_sm100.cuh"
@@ -311,6 +313,25 @@ Dec4Plan dec4_plan(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, int 
                      : dec4_plan_for<64, 4>(B, Hkv, rows, Tq, max_seqlen_k, window);
 }
 
+// The workspace of a plan that has one.
+gqa_status dec4_workspace(gqa::Dec4Params& p, const Dec4Plan& r, void* workspace, size_t workspace_bytes) {
+    if (r.bytes == 0) return GQA_OK;
+    if (!aligned(workspace, 256) || workspace_bytes < r.bytes) return GQA_ERR_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    p.part = reinterpret_cast<float*>(ws + r.part);
+    p.part_lse = reinterpret_cast<float*>(ws + r.lse);
+    p.ends = reinterpret_cast<int2*>(ws + r.ends);
+    p.runs = r.ctas * r.warps;
+    return GQA_OK;
+}
+
+template <int D, int NT>
+gqa_status launch_dec4_merge(const gqa::Dec4Params& p, cudaStream_t stream) {
+    const dim3 grid((unsigned)p.B, (unsigned)(p.Hq * p.Tq));
+    gqa::gqa_decode_kv4_merge_kernel<D, NT><<<grid, 32 * gqa::kD4MergeWarps, 0, stream>>>(p);
+    return launched(cudaGetLastError());
+}
+
 template <int D, int NT>
 gqa_status launch_dec4(const gqa::Dec4Params& p, const Dec4Plan& r, cudaStream_t stream) {
     using C = gqa::Dec4Cfg<D, NT>;
@@ -330,9 +351,18 @@ gqa_status launch_dec4(const gqa::Dec4Params& p, const Dec4Plan& r, cudaStream_t
     cfg.attrs = &attr;
     cfg.numAttrs = r.cluster ? 1 : 0;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess || r.cluster) return launched(e);
-    const dim3 grid((unsigned)p.B, (unsigned)(p.Hq * p.Tq));
-    gqa::gqa_decode_kv4_merge_kernel<D, NT><<<grid, 32 * gqa::kD4MergeWarps, 0, stream>>>(p);
-    return launched(cudaGetLastError());
+    return launch_dec4_merge<D, NT>(p, stream);
+}
+
+// f with D and the N tiles as constants.
+template <class F>
+gqa_status dec4_dispatch(int D, int nt, F f) {
+    const auto of = [&](auto d) {
+        return nt == 1   ? f(d, std::integral_constant<int, 1>{})
+               : nt == 2 ? f(d, std::integral_constant<int, 2>{})
+                         : f(d, std::integral_constant<int, 4>{});
+    };
+    return D == 128 ? of(std::integral_constant<int, 128>{}) : of(std::integral_constant<int, 64>{});
 }
 
 }  // namespace
@@ -501,13 +531,7 @@ gqa_status gqa_attn_decode_kv4(const void* q, const void* k_pool, const void* v_
     if ((st = check_kv4_pool(k_pool, k_layout, num_pages, Hkv, page_size, D, &p.k_sb, &p.k_sh)) != GQA_OK) return st;
     if ((st = check_kv4_pool(v_pool, v_layout, num_pages, Hkv, page_size, D, &p.v_sb, &p.v_sh)) != GQA_OK) return st;
     const Dec4Plan r = dec4_plan(B, Hq, Hkv, Tq, max_seqlen_k, D, window);
-    if (r.bytes > 0) {
-        if (!aligned(workspace, 256) || workspace_bytes < r.bytes) return GQA_ERR_WORKSPACE;
-        char* ws = static_cast<char*>(workspace);
-        p.part = reinterpret_cast<float*>(ws + r.part);
-        p.part_lse = reinterpret_cast<float*>(ws + r.lse);
-        p.ends = reinterpret_cast<int2*>(ws + r.ends);
-    }
+    if ((st = dec4_workspace(p, r, workspace, workspace_bytes)) != GQA_OK) return st;
     p.q = static_cast<const bf16*>(q);
     p.o = static_cast<bf16*>(o);
     p.k = static_cast<const uint8_t*>(k_pool);
@@ -529,13 +553,30 @@ gqa_status gqa_attn_decode_kv4(const void* q, const void* k_pool, const void* v_
     p.timeout_ns = gqa::kWaitTimeoutNs;
     if ((p.err = gqa::device_error_ptr()) == nullptr) return GQA_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (D == 128)
-        return r.nt == 1   ? launch_dec4<128, 1>(p, r, s)
-               : r.nt == 2 ? launch_dec4<128, 2>(p, r, s)
-                           : launch_dec4<128, 4>(p, r, s);
-    return r.nt == 1   ? launch_dec4<64, 1>(p, r, s)
-           : r.nt == 2 ? launch_dec4<64, 2>(p, r, s)
-                       : launch_dec4<64, 4>(p, r, s);
+    return dec4_dispatch(D, r.nt, [&](auto d, auto nt) { return launch_dec4<d, nt>(p, r, s); });
+}
+
+gqa_status gqa_testing_decode_kv4_merge(void* o, const int* seqlens_k, int B, int Hq, int Hkv, int Tq, int max_seqlen_k,
+                                        int D, void* workspace, size_t workspace_bytes, int* out_runs, void* stream) {
+    gqa_status st = check_dec4(B, Hq, Hkv, Tq, max_seqlen_k, D, 0);
+    if (st != GQA_OK) return st;
+    if (!aligned(o, 16) || !aligned(seqlens_k, 4) || out_runs == nullptr) return GQA_ERR_INVALID_ARGUMENT;
+    const Dec4Plan r = dec4_plan(B, Hq, Hkv, Tq, max_seqlen_k, D, 0);
+    if (r.bytes == 0) return GQA_ERR_UNSUPPORTED;  // merged without the workspace
+    gqa::Dec4Params p{};
+    if ((st = dec4_workspace(p, r, workspace, workspace_bytes)) != GQA_OK) return st;
+    *out_runs = p.runs;
+    p.o = static_cast<bf16*>(o);
+    p.seqlens = seqlens_k;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.Tq = Tq;
+    p.n_rc = r.n_rc;
+    p.capacity = max_seqlen_k;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dec4_dispatch(D, r.nt, [&](auto d, auto nt) { return launch_dec4_merge<d, nt>(p, s); });
 }
 
 }  // extern "C"

@@ -66,6 +66,20 @@ GQA_API gqa_status gqa_testing_fwd_split_plan(int B, int Hq, int Hkv, int Tq, in
                                               int* out_slices, long long* out_whole, long long* out_split,
                                               long long* out_units);
 
+/*
+ * Launches the merge of gqa_attn_decode_kv4 alone, for calls of these sizes that cut units between
+ * runs, over a workspace as it is: fp32 partial outputs [2 * runs, rows, D], their log2-domain
+ * log-sum-exps [2 * runs, rows], each padded to 256 bytes, and last int32 pairs [B * Hkv * chunks],
+ * the first and the last run of each unit's pieces (equal: nothing to merge). Piece slot 2 * run + 1
+ * starts a unit, slot 2 * run does not; rows is 8, 16 or 32, and chunks cover the Hq / Hkv * Tq rows of a
+ * KV head. A pair outside [0, runs) or out of order is left alone: that is how a decode ends whose
+ * wait ran out before it had written the pair. *out_runs (host memory) gets the number of
+ * runs. Returns GQA_ERR_UNSUPPORTED for sizes that need no workspace, else as gqa_attn_decode_kv4.
+ */
+GQA_API gqa_status gqa_testing_decode_kv4_merge(void* o, const int* seqlens_k, int B, int Hq, int Hkv, int Tq,
+                                                int max_seqlen_k, int D, void* workspace, size_t workspace_bytes,
+                                                int* out_runs, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,4 +1,6 @@
 """What the operators around the paged cache refuse at the ends of their ranges, without a GPU."""
+import ctypes
+
 import pytest
 
 
@@ -16,3 +18,15 @@ def test_plan_refuses_tables_of_more_pages_than_it_counts(gqa, S, max_pages, pag
     """Every request may give all its pages back at once: their number has to fit 32 bits."""
     st = gqa.gqa_paged_plan(P, P, P, P, P, P, 2 * P, 2 * P, 2 * P, 2 * P, 2 * P, S, max_pages, page, 1000, 1000, 64)
     assert st == gqa.GQA_ERR_UNSUPPORTED
+
+
+def test_merge_hook_refuses_what_the_decode_refuses(gqa):
+    f = ctypes.CDLL(gqa.library_path()).gqa_testing_decode_kv4_merge
+    f.argtypes = [ctypes.c_void_p] * 2 + [ctypes.c_int] * 6 + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]
+    runs = ctypes.c_int()
+    many = (64, 32, 8, 1, 32768, 128)
+    assert f(P, P, *many, None, 0, ctypes.byref(runs), None) == gqa.GQA_ERR_WORKSPACE
+    assert f(P, P, *many, P, 1 << 20, ctypes.byref(runs), None) == gqa.GQA_ERR_WORKSPACE
+    assert f(None, P, *many, P, 1 << 30, ctypes.byref(runs), None) == gqa.GQA_ERR_INVALID_ARGUMENT
+    assert f(P, P, *many, P, 1 << 30, None, None) == gqa.GQA_ERR_INVALID_ARGUMENT
+    assert f(P, P, 1, 32, 8, 1, 4099, 128, P, 1 << 30, ctypes.byref(runs), None) == gqa.GQA_ERR_UNSUPPORTED

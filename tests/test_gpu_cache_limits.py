@@ -1,5 +1,6 @@
 """The operators around the paged cache at the ends of what their arguments allow."""
-import numpy as np
+import ctypes
+
 import pytest
 
 from tests.gpu_util import torch_mod
@@ -41,3 +42,43 @@ def test_plan_of_as_many_tokens_as_fit_32_bits(gqa, in_place):
         assert torch.equal(p.positions[lo:hi].long(), want)
         assert torch.equal(p.slots[lo:hi].long(), (pages - 1 - want // page) * page + want % page)
     assert (p.positions[total:] == 0).all() and (p.slots[total:] == -1).all()
+
+
+def test_decode_kv4_merge_follows_only_runs_of_its_workspace(gqa):
+    """The merge over units whose pieces' runs are not what a decode leaves: numbers a workspace may
+    hold where a wait ran out. Those rows stay as they are, the others are merged."""
+    torch = torch_mod()
+    B, Hq, Hkv, Tq, longest, D, rows = 64, 32, 8, 1, 32768, 128, 8
+    lib = ctypes.CDLL(gqa.library_path())
+    lib.gqa_testing_decode_kv4_merge.argtypes = ([ctypes.c_void_p] * 2 + [ctypes.c_int] * 6
+                                                 + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p])
+    nbytes = gqa.gqa_attn_decode_kv4_workspace_bytes(B, Hq, Hkv, Tq, longest, D)
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+    lens = torch.full((B,), longest, dtype=torch.int32, device="cuda")
+    out = torch.full((B, Hq, Tq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    runs = ctypes.c_int()
+
+    def merge():
+        return lib.gqa_testing_decode_kv4_merge(out.data_ptr(), lens.data_ptr(), B, Hq, Hkv, Tq, longest, D, ws.data_ptr(),
+                                                nbytes, ctypes.byref(runs), torch.cuda.current_stream().cuda_stream)
+
+    assert merge() == gqa.GQA_OK   # all pairs are (0, 0): nothing to merge
+    torch.cuda.synchronize()
+    assert (out == 7).all()
+    n = runs.value
+    ends = ws[nbytes - 8 * B * Hkv:].view(torch.int32).view(B, Hkv, 2)
+    parts = ws[:2 * n * rows * D * 4].view(torch.float32).view(n, 2, rows, D)   # log-sum-exps of 0: equal weights
+    for run, slot, value in ((3, 1, 1.0), (4, 0, 2.0), (5, 0, 6.0), (n - 2, 1, 4.0), (n - 1, 0, 5.0)):
+        parts[run, slot] = value
+    bad = [(-1, 3), (-2 ** 31, 2 ** 31 - 1), (5, 3), (n - 1, n), (0, 2 ** 31 - 1), (2 ** 31 - 1, 0), (n, n + 1), (-5, -2)]
+    for h, pair in enumerate(bad):
+        ends[1, h] = torch.tensor(pair, dtype=torch.int64).int()
+    ends[0, 0], ends[2, 7] = torch.tensor([3, 5]), torch.tensor([n - 2, n - 1])
+    lens[2] = longest + 1     # such a sequence has no output, whatever its pairs say
+    ends[63, 0], lens[62], ends[62, 0] = torch.tensor([n - 2, n - 1]), -1, torch.tensor([3, 5])
+    assert merge() == gqa.GQA_OK
+    torch.cuda.synchronize()
+    assert gqa.gqa_get_device_error() == gqa.GQA_OK
+    want = torch.full_like(out, 7.0)
+    want[0, :4], want[63, :4] = 3.0, 4.5
+    assert torch.equal(out, want)
