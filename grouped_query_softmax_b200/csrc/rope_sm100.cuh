@@ -225,19 +225,20 @@ __device__ __forceinline__ RopeAt rope_at(const RopeParams& p, unsigned tok, int
     a.h1 = min(a.h0 + p.heads_per_team, p.x[which].H);
     return a;
 }
-// The angles of a team's token in the lane's four pairs (1, 0 where nothing turns); false, with
-// an error set, if its position is outside the tables.
+// The angles of a team's token in the lane's four pairs (1, 0 where nothing turns, as in values);
+// false, with an error set, if its position is outside the tables: then a token's value row is left
+// out with its key row.
 __device__ __forceinline__ bool rope_angles(const RopeParams& p, const RopeAt& a, const RopeLane& l, uint64_t (&c)[2],
                                             uint64_t (&s)[2]) {
     c[0] = c[1] = rope2(1.f, 1.f);
     s[0] = s[1] = rope2(0.f, 0.f);
-    if (p.cos == nullptr || a.which == 2) return true;
+    if (p.cos == nullptr) return true;
     const int pos = p.positions ? __ldg(p.positions + a.b * p.pos_sb + a.t) : a.t;
     if ((unsigned)pos >= (unsigned)p.n_positions) {
         if (a.live) atomicOr(p.err, kDevErrBadSeqlens);
         return false;
     }
-    if (l.angle >= 0) {
+    if (l.angle >= 0 && a.which != 2) {
         const long long at = (long long)pos * (p.rot >> 1) + l.angle;
         const float4 x = __ldg(reinterpret_cast<const float4*>(p.cos + at)), y = __ldg(reinterpret_cast<const float4*>(p.sin + at));
         c[0] = rope2(x.x, x.y), c[1] = rope2(x.z, x.w);

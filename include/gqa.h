@@ -505,7 +505,8 @@ GQA_API gqa_status gqa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, 
  * slots[t] / page_size (gqa_paged_plan's slots). k_pool and v_pool are the bf16 pools of
  * gqa_attn_decode_varlen and gqa_attn_fwd_varlen_paged (b = pool page, t = row of the page).
  * A negative slot writes no row (the query is still written); a slot past the pool writes none
- * either and is reported like a bad position. Slots of one call are distinct: of two equal ones,
+ * either and is reported like a bad position, which leaves the token's query, key and value rows
+ * unwritten. Slots of one call are distinct: of two equal ones,
  * the row holds a mixture. N = 0 launches nothing.
  */
 GQA_API gqa_status gqa_qk_norm_rope_append(const void* q, const void* k, const void* v, void* q_out, void* k_pool,

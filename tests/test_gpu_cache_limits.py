@@ -3,7 +3,9 @@ import ctypes
 
 import pytest
 
-from tests.gpu_util import torch_mod
+import gqa_inputs as gi
+from tests import cache_ref as ref
+from tests.gpu_util import to_dev, torch_mod
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +84,27 @@ def test_decode_kv4_merge_follows_only_runs_of_its_workspace(gqa):
     want = torch.full_like(out, 7.0)
     want[0, :4], want[63, :4] = 3.0, 4.5
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("pool_layout,rot", [("NHD", 64), ("HND", 32)])
+def test_append_leaves_all_rows_of_a_bad_position(gqa, pool_layout, rot):
+    """A token outside the angle tables: neither its key nor its value row is written, nor its query."""
+    torch = torch_mod()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    q, k, v = (to_dev(gi.normal_bf16(101 + i, i, (6, h, 64))) for i, h in enumerate((4, 2, 2)))
+    cos, sin = (torch.tensor(t, device="cuda") for t in ref.angles(10, rot))
+    shape = (3, 16, 2, 64) if pool_layout == "NHD" else (3, 2, 16, 64)
+    new = lambda: [torch.full(shape, 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)] + [torch.full_like(q, 9.0)]
+    slots = i32([5, 20, 40, 1, -1, 30])
+    good, got = new(), new()
+    for out, positions in ((good, [0, 1, 2, 3, 4, 5]), (got, [0, 10, 2, -1, 4, 5])):
+        gqa.qk_norm_rope_append(q, k, v, out[0], out[1], slots, cos=cos, sin=sin, positions=i32(positions),
+                                pool_layout=pool_layout, q_out=out[2])
+        torch.cuda.synchronize()
+        assert gqa.gqa_get_device_error() == (gqa.GQA_OK if out is good else gqa.GQA_ERR_INVALID_ARGUMENT)
+    for want, have in zip(good[:2], got[:2]):
+        for slot in (20, 1):
+            want[(slot // 16, slot % 16) if pool_layout == "NHD" else (slot // 16, slice(None), slot % 16)] = 9.0
+        assert torch.equal(want, have)
+    good[2][[1, 3]] = 9.0
+    assert torch.equal(good[2], got[2])
