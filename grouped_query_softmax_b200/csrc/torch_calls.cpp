@@ -88,6 +88,12 @@ void has_shape(const Arg& a, Sizes shape) {
 void is_int32(const Arg& a) {
     if (a->scalar_type() != at::kInt || !a->is_contiguous()) type_error(std::string(a.name) + " must be a contiguous int32 tensor");
 }
+// A workspace's bytes are its elements': an expanded tensor has fewer behind it.
+Arg workspace(PyObject* o) {
+    const Arg a = tensor_or_none(o, "workspace");
+    if (a && !a->is_contiguous()) value_error("workspace must be contiguous");
+    return a;
+}
 // Layout of a bf16 operand [B, H, T, D], or [T, H, D] with three axes.
 gqa_layout rows(const Arg& a, int dims) {
     if (a->scalar_type() != at::kBFloat16) type_error(std::string(a.name) + " must be a bf16 tensor");
@@ -315,7 +321,7 @@ PyObject* py_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         has_shape(gq, x.q->sizes());
         has_shape(gk, x.k->sizes());
         const Rope rope(a + 4, x.D, x.B, x.T);
-        const Arg oq = tensor_or_none(a[11], "dq"), ok = tensor_or_none(a[12], "dk"), ws = tensor_or_none(a[13], "workspace");
+        const Arg oq = tensor_or_none(a[11], "dq"), ok = tensor_or_none(a[12], "dk"), ws = workspace(a[13]);
         const int device = on_device({gq, gk, x.q, x.k, oq, ok, ws, rope.q_weight, rope.k_weight, rope.cos, rope.sin, rope.positions});
         const Out dq(oq, x.q, 4), dk(ok, x.k, 4);
         const int B = to_int(x.B, "q"), T = to_int(x.T, "q"), Hq = to_int(x.Hq, "q"), Hkv = to_int(x.Hkv, "k"), D = to_int(x.D, "q");
@@ -453,7 +459,7 @@ PyObject* py_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         has_shape(lens, {q->size(0)});
         is_int32(table);
         if (table->dim() != 2 || table->size(0) != q->size(0)) value_error("block_table must be [B, max_pages]");
-        const Arg given = tensor_or_none(a[8], "out"), ws = tensor_or_none(a[9], "workspace");
+        const Arg given = tensor_or_none(a[8], "out"), ws = workspace(a[9]);
         const int device = on_device({q, kp, vp, lens, table, given, ws});
         at::Tensor out;
         if (given) {

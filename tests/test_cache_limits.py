@@ -30,3 +30,17 @@ def test_merge_hook_refuses_what_the_decode_refuses(gqa):
     assert f(None, P, *many, P, 1 << 30, ctypes.byref(runs), None) == gqa.GQA_ERR_INVALID_ARGUMENT
     assert f(P, P, *many, P, 1 << 30, None, None) == gqa.GQA_ERR_INVALID_ARGUMENT
     assert f(P, P, 1, 32, 8, 1, 4099, 128, P, 1 << 30, ctypes.byref(runs), None) == gqa.GQA_ERR_UNSUPPORTED
+
+
+def test_workspaces_that_claim_more_bytes_than_they_have_are_refused(gqa):
+    """An expanded tensor's elements share memory: its size is not what a kernel may write."""
+    torch = pytest.importorskip("torch")
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    pool = torch.zeros((5, 2, 16, 36), dtype=torch.uint8)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 30), torch.zeros(1 << 12, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            gqa.attn_decode_kv4(bf(2, 4, 64), pool, pool, i32(2), i32(2, 4), workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            gqa.qk_norm_rope_bwd(bf(1, 4, 3, 64), bf(1, 2, 3, 64), bf(1, 4, 3, 64), bf(1, 2, 3, 64), q_weight=bf(64),
+                                 k_weight=bf(64), workspace=ws)
