@@ -516,7 +516,12 @@ PyMethodDef methods[] = {
     GQA_METHOD("kv4_gather", py_kv4_gather),       GQA_METHOD("attn_decode_kv4", py_decode),
     {nullptr, nullptr, 0, nullptr},
 };
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+#ifndef GQA_BUILT_FOR
+#define GQA_BUILT_FOR "built for an unknown torch"
+#endif
+// The module's documentation; the build looks it up in the file to see whether the module is of the
+// installed versions.
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", GQA_BUILT_FOR, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
