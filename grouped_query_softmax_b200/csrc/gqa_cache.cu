@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -325,6 +326,31 @@ gqa_status dec4_workspace(gqa::Dec4Params& p, const Dec4Plan& r, void* workspace
     return GQA_OK;
 }
 
+std::atomic<int> g_dec4_largest{16};  // CTAs of a cluster, for tests of the smaller forms
+
+// Clusters above the portable eight CTAs need a GPC with that many SMs free to the process, which a
+// partitioned device may not have: the largest power of two that this kernel can have, asked once a
+// device. The kernel takes any size.
+template <int D, int NT>
+int dec4_largest_cluster(cudaLaunchConfig_t cfg) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 8;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cfg.gridDim = dim3(16);
+        cfg.attrs = nullptr;
+        cfg.numAttrs = 0;
+        if (cudaOccupancyMaxPotentialClusterSize(&n, gqa::gqa_decode_kv4_kernel<D, NT, true>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        n = n >= 16 ? 16 : 8;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 template <int D, int NT>
 gqa_status launch_dec4_merge(const gqa::Dec4Params& p, cudaStream_t stream) {
     const dim3 grid((unsigned)p.B, (unsigned)(p.Hq * p.Tq));
@@ -339,15 +365,23 @@ gqa_status launch_dec4(const gqa::Dec4Params& p, const Dec4Plan& r, cudaStream_t
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
     if (e == cudaSuccess && r.cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return GQA_ERR_CUDA;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = r.cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)r.ctas);
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kBytes;
     cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = r.cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    if (r.cluster > 1) {
+        int most = g_dec4_largest.load(std::memory_order_relaxed);
+        if (r.cluster > 8) most = std::min(most, dec4_largest_cluster<D, NT>(cfg));
+        if (r.cluster > most) {
+            attr.val.clusterDim.x = most;
+            cfg.gridDim = dim3((unsigned)(r.ctas / r.cluster * most));
+        }
+    }
     cfg.attrs = &attr;
     cfg.numAttrs = r.cluster ? 1 : 0;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess || r.cluster) return launched(e);
@@ -554,6 +588,12 @@ gqa_status gqa_attn_decode_kv4(const void* q, const void* k_pool, const void* v_
     if ((p.err = gqa::device_error_ptr()) == nullptr) return GQA_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return dec4_dispatch(D, r.nt, [&](auto d, auto nt) { return launch_dec4<d, nt>(p, r, s); });
+}
+
+gqa_status gqa_testing_decode_kv4_largest_cluster(int ctas) {
+    if (ctas < 1 || ctas > 16 || (ctas & (ctas - 1))) return GQA_ERR_INVALID_ARGUMENT;
+    g_dec4_largest.store(ctas, std::memory_order_relaxed);
+    return GQA_OK;
 }
 
 gqa_status gqa_testing_decode_kv4_merge(void* o, const int* seqlens_k, int B, int Hq, int Hkv, int Tq, int max_seqlen_k,

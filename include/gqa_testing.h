@@ -80,6 +80,13 @@ GQA_API gqa_status gqa_testing_decode_kv4_merge(void* o, const int* seqlens_k, i
                                                 int max_seqlen_k, int D, void* workspace, size_t workspace_bytes,
                                                 int* out_runs, void* stream);
 
+/*
+ * Makes later gqa_attn_decode_kv4 calls that take a cluster of CTAs a unit launch clusters of at
+ * most `ctas` (1, 2, 4, 8 or 16; 16 is the default), as on a device that cannot hold larger ones.
+ * Process-wide; touches no GPU. Returns GQA_ERR_INVALID_ARGUMENT for other values.
+ */
+GQA_API gqa_status gqa_testing_decode_kv4_largest_cluster(int ctas);
+
 #ifdef __cplusplus
 }
 #endif

@@ -44,3 +44,8 @@ def test_workspaces_that_claim_more_bytes_than_they_have_are_refused(gqa):
         with pytest.raises(ValueError, match="workspace"):
             gqa.qk_norm_rope_bwd(bf(1, 4, 3, 64), bf(1, 2, 3, 64), bf(1, 4, 3, 64), bf(1, 2, 3, 64), q_weight=bf(64),
                                  k_weight=bf(64), workspace=ws)
+
+
+def test_largest_cluster_hook_takes_powers_of_two(gqa):
+    f = ctypes.CDLL(gqa.library_path()).gqa_testing_decode_kv4_largest_cluster
+    assert [f(n) for n in (0, 3, 32, -1)] == [gqa.GQA_ERR_INVALID_ARGUMENT] * 4 and f(8) == f(16) == 0

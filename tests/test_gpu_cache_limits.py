@@ -5,7 +5,8 @@ import pytest
 
 import gqa_inputs as gi
 from tests import cache_ref as ref
-from tests.gpu_util import to_dev, torch_mod
+from tests.gpu_util import from_dev, to_dev, torch_mod
+from tests.test_gpu_cache import _kv4_pools, _near
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +109,25 @@ def test_append_leaves_all_rows_of_a_bad_position(gqa, pool_layout, rot):
         assert torch.equal(want, have)
     good[2][[1, 3]] = 9.0
     assert torch.equal(good[2], got[2])
+
+
+@pytest.mark.parametrize("largest", [1, 2, 4, 8, 16])
+@pytest.mark.parametrize("Hq,Hkv,Tq,D,lens,window", [(8, 2, 1, 128, [4099], 0), (16, 2, 2, 64, [3000, 0, 1, 777], 0),
+                                                     (32, 1, 1, 128, [2500, 40], 1000)])
+def test_decode_kv4_in_smaller_clusters(gqa, largest, Hq, Hkv, Tq, D, lens, window):
+    """Cases that take clusters of 16 CTAs, on a device that would hold fewer."""
+    torch = torch_mod()
+    lib = ctypes.CDLL(gqa.library_path())
+    kp, vp, table = _kv4_pools(lens, Hkv, D, 64, 111, window, Tq)
+    q = gi.normal_bf16(112, gi.TENSOR_Q, (len(lens), Hq, Tq, D))
+    dev = lambda x: torch.tensor(x, device="cuda")
+    try:
+        assert lib.gqa_testing_decode_kv4_largest_cluster(largest) == 0
+        o = gqa.attn_decode_kv4(to_dev(q), dev(kp), dev(vp), torch.tensor(lens, dtype=torch.int32, device="cuda"), dev(table),
+                                window=window)
+        torch.cuda.synchronize()
+    finally:
+        assert lib.gqa_testing_decode_kv4_largest_cluster(16) == 0
+    assert gqa.gqa_get_device_error() == gqa.GQA_OK
+    want, tol = ref.decode_kv4(q, kp, vp, lens, table, window)
+    _near(from_dev(o), want, tol, f"clusters of at most {largest}")
