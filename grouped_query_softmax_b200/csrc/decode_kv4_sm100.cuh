@@ -117,9 +117,13 @@ __device__ __forceinline__ Dec4Seq dec4_seq(const Dec4Params& p, int b) {
     return s;
 }
 
-// Start of run i when `total` tiles are cut into `runs`; total is below 2^52 (checked on the host)
-// and runs at most a few thousand.
-__device__ __forceinline__ unsigned long long dec4_cut(unsigned long long total, unsigned i, unsigned runs) {
+// Runs that `total` tiles are cut into, of at most `places`, and the start of run i; total is below
+// 2^52 (checked on the host) and runs at most a few thousand.
+__host__ __device__ __forceinline__ unsigned dec4_runs(unsigned long long total, unsigned places) {
+    const unsigned long long most = (total + kD4MinRun - 1) / kD4MinRun;
+    return most < places ? (unsigned)most : places;
+}
+__host__ __device__ __forceinline__ unsigned long long dec4_cut(unsigned long long total, unsigned i, unsigned runs) {
     if (total < 1u << 19 && runs <= 1u << 13) return (unsigned)total * i / runs;  // i <= runs: 32 bits do
     return total * i / runs;
 }
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
             for (int w = 0; w < warp; ++w) lo += ctl->sums[w];
             for (int w = 0; w < kWarps; ++w) before += ctl->sums[w];
             if (one_pass) total = before;
-            runs = (unsigned)min((unsigned long long)gridDim.x * kWarps, (total + kD4MinRun - 1) / kD4MinRun);
+            runs = dec4_runs(total, gridDim.x * kWarps);
             for (int w = 0; w < kWarps; ++w) {
                 const unsigned r = w * gridDim.x + blockIdx.x;
                 const unsigned long long first = r < runs ? dec4_cut(total, r, runs) : total;

@@ -590,6 +590,16 @@ gqa_status gqa_attn_decode_kv4(const void* q, const void* k_pool, const void* v_
     return dec4_dispatch(D, r.nt, [&](auto d, auto nt) { return launch_dec4<d, nt>(p, r, s); });
 }
 
+gqa_status gqa_testing_decode_kv4_cut(unsigned long long total, int places, int i, int* out_runs,
+                                      unsigned long long* out_start) {
+    if (total == 0 || total >= 1ULL << 52 || places <= 0 || places > 1 << 12 || i < 0 || out_runs == nullptr || out_start == nullptr)
+        return GQA_ERR_INVALID_ARGUMENT;
+    *out_runs = (int)gqa::dec4_runs(total, (unsigned)places);
+    if (i > *out_runs) return GQA_ERR_INVALID_ARGUMENT;
+    *out_start = gqa::dec4_cut(total, (unsigned)i, (unsigned)*out_runs);
+    return GQA_OK;
+}
+
 gqa_status gqa_testing_decode_kv4_largest_cluster(int ctas) {
     if (ctas < 1 || ctas > 16 || (ctas & (ctas - 1))) return GQA_ERR_INVALID_ARGUMENT;
     g_dec4_largest.store(ctas, std::memory_order_relaxed);

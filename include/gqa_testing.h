@@ -81,6 +81,15 @@ GQA_API gqa_status gqa_testing_decode_kv4_merge(void* o, const int* seqlens_k, i
                                                 int* out_runs, void* stream);
 
 /*
+ * How gqa_attn_decode_kv4 cuts the tiles of all units between its warps, for host-side tests:
+ * `total` tiles (below 2^52) over at most `places` warps (at most 4096) make *out_runs runs, and
+ * run i starts at tile *out_start (i == *out_runs: one past the last). Touches no GPU. Returns
+ * GQA_ERR_INVALID_ARGUMENT for other values, a larger i or a null pointer.
+ */
+GQA_API gqa_status gqa_testing_decode_kv4_cut(unsigned long long total, int places, int i, int* out_runs,
+                                              unsigned long long* out_start);
+
+/*
  * Makes later gqa_attn_decode_kv4 calls that take a cluster of CTAs a unit launch clusters of at
  * most `ctas` (1, 2, 4, 8 or 16; 16 is the default), as on a device that cannot hold larger ones.
  * Process-wide; touches no GPU. Returns GQA_ERR_INVALID_ARGUMENT for other values.
