@@ -61,6 +61,18 @@ int sm_count() {
 }
 
 // ---------------------------------------------------------------- plan
+// Threads that a step keeps busy once: four tokens each, or one page that it may take or give back.
+long long paged_work(const gqa::PagedPlanParams& p) {
+    return ((long long)p.max_tokens + 3) / 4 + p.max_tokens / p.page_size + p.S;
+}
+// Blocks of 256 threads for few requests, whose scans then cost less, while at most two rounds of
+// them do the work; else of 1024. us with 256 / 1024: 64 requests with 1024 tokens 3.6 / 4.5, 262 144
+// tokens 5.1 / 5.5, 524 288 tokens 7.8 / 5.5, in place 16 384 tokens 5.5 / 6.0, 32 768 tokens 8.1 / 6.1;
+// 256 requests with 65 536 tokens 4.2 / 5.5; 768 requests with 768 tokens 7.5 / 7.0.
+bool paged_few(const gqa::PagedPlanParams& p, int ctas) {
+    return p.S <= gqa::kPagedFewSeqs && paged_work(p) <= 2LL * gqa::kPagedFewThreads * ctas;
+}
+
 template <int kThreads, bool kCluster>
 gqa_status paged_plan(const gqa::PagedPlanParams& p, cudaStream_t stream) {
     const auto kernel = gqa::gqa_paged_plan_kernel<kThreads, kCluster>;
@@ -69,16 +81,14 @@ gqa_status paged_plan(const gqa::PagedPlanParams& p, cudaStream_t stream) {
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)gqa::paged_plan_smem(gqa::kPagedMaxSeqs)) != cudaSuccess)
         return GQA_ERR_CUDA;
-    // four tokens a thread, and one page that the step may take or give back
-    const long long work = ((long long)p.max_tokens + 3) / 4 + p.max_tokens / p.page_size + p.S;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     if (kCluster)
-        cfg.gridDim.x = attr.val.clusterDim.x = p.max_tokens > gqa::kPagedTokensAlone ? gqa::kPagedCluster : 1;
+        cfg.gridDim.x = attr.val.clusterDim.x = gqa::kPagedCluster;
     else
-        cfg.gridDim.x = (unsigned)std::min<long long>((work + kThreads - 1) / kThreads, sm_count());
+        cfg.gridDim.x = (unsigned)std::min<long long>((paged_work(p) + kThreads - 1) / kThreads, sm_count());
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -123,10 +133,13 @@ gqa_status rope_params(gqa::RopeParams& p, const gqa_rope* r, int B, int T, int 
 
 // Heads of a token that one team of D/8 lanes takes in turn: its loads of the angles and weights
 // serve that many rows, so a large launch takes `many`; a small one takes the four it has in
-// flight at a time, to spread over the SMs.
+// flight at a time, to spread over the SMs. The sides meet near 512 lanes an SM. Forward, us with 4 / 16:
+// 32 + 8 heads of 128, 256 tokens 3.2 / 5.5, 1536 tokens 6.9 / 7.1, 2048 tokens 8.8 / 8.2, 6144 tokens 23.9 / 20.1;
+// 6 + 2 heads of 64, 4096 tokens 3.9 / 4.0, 12 288 tokens 7.2 / 6.9. Backward, with 4 / 8: 32 + 8 heads of
+// 128, 256 tokens 6.6 / 7.0, 1024 tokens 11.4 / 11.5, 3584 tokens 25.6 / 22.7; 32 + 1 heads, 1024 tokens 9.7 / 8.9.
 int rope_heads_per_team(long long tokens, int heads, int D, int many, int sms) {
     const long long lanes = tokens * ((heads + many - 1) / many) * (D / 8);
-    return lanes >= (long long)sms * 2048 ? many : gqa::kRopeUnroll;
+    return lanes >= (long long)sms * 512 ? many : gqa::kRopeUnroll;
 }
 // Heads, split into blocks; false if there are more blocks than a grid's y extent.
 bool rope_blocks(gqa::RopeParams& p, int heads_per_team) {
@@ -230,8 +243,10 @@ gqa_status kv4_rows(bool append, const void* k, const void* v, const void* k_poo
     p.num_pages = num_pages;
     if ((p.err = gqa::device_error_ptr()) == nullptr) return GQA_ERR_CUDA;
     const int per = gqa::kKv4Threads / (D / 8);
-    // many rows: eight heads a team, to spread its set-up; few: the four it has in flight at a time
-    p.heads_per_team = 2LL * N * ((Hkv + 7) / 8) * (D / 8) >= (long long)sm_count() * 2048 ? 8 : gqa::kKv4Unroll;
+    // Many rows: eight heads a team, to spread its set-up; few: the four it has in flight at a time. us with 4 / 8,
+    // written and read, 8 heads of 128: 256 tokens 4.2 / 5.6, 4096 tokens 10.2 / 10.3, 6144 tokens 14.0 / 13.7, 16 384
+    // tokens 33.0 / 30.1; 8 heads of 64, 10 240 tokens 12.2 / 12.0.
+    p.heads_per_team = 2LL * N * ((Hkv + 7) / 8) * (D / 8) >= (long long)sm_count() * 1024 ? 8 : gqa::kKv4Unroll;
     p.blocks = (Hkv + p.heads_per_team - 1) / p.heads_per_team;
     if (2LL * p.blocks > 65535) return GQA_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)((N + (long long)per - 1) / per), (unsigned)(2 * p.blocks));
@@ -423,7 +438,8 @@ gqa_status gqa_paged_plan(const int* seqlens, const int* keep, const int* new_to
     const bool in_place =
         seqlens_out == seqlens || seqlens_out == keep || seqlens_out == new_tokens || free_count_out == free_count;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (S <= gqa::kPagedFewSeqs) return in_place ? paged_plan<gqa::kPagedFewSeqs, true>(p, s) : paged_plan<gqa::kPagedFewSeqs, false>(p, s);
+    if (paged_few(p, in_place ? gqa::kPagedCluster : sm_count()))
+        return in_place ? paged_plan<gqa::kPagedFewThreads, true>(p, s) : paged_plan<gqa::kPagedFewThreads, false>(p, s);
     return in_place ? paged_plan<1024, true>(p, s) : paged_plan<1024, false>(p, s);
 }
 
