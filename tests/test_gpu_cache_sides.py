@@ -115,3 +115,78 @@ def test_plan_of_many_tokens(gqa, in_place, S, per, padding):
     for got, want in ((p.seqlens_k, after), (p.cu_seqlens, cu), (p.positions, pos), (p.slots, slots), (td, t2), (p.free_count, [c2])):
         np.testing.assert_array_equal(got.cpu().numpy(), want)
     np.testing.assert_array_equal(fd.cpu().numpy()[:c2], f2[:c2])
+
+
+@pytest.mark.parametrize("side", ["q_weight", "k_weight"])
+@pytest.mark.parametrize("case", [(2, 37, 6, 2, 64, 32, True, True, False), (1, 1300, 32, 8, 128, 128, False, True, True)], ids=str)
+def test_norm_on_one_side_only(gqa, case, side):
+    """A weight for the queries or the keys alone: the other side is rotated as it is, and has no
+    weight gradient; its inputs are not read by the backward pass."""
+    torch = torch_mod()
+    B, T, Hq, Hkv, D, rot, inter, _, fp32 = case
+    qkv, w, cos, sin, pos = _rope_inputs(case, 201)
+    w = {n: v if n == side else None for n, v in w.items()}
+    dz = [gi.normal_bf16(202 + i, gi.TENSOR_DO, (B, h, T, D)) for i, h in enumerate((Hq, Hkv))]
+    d = to_dev(qkv).transpose(1, 2)
+    x = [d[:, :Hq], d[:, Hq:Hq + Hkv]]
+    how = dict(_dev_weights(w, fp32), cos=_dev(cos), sin=_dev(sin), positions=_dev(pos), interleaved=inter, eps=1e-5)
+    z = gqa.qk_norm_rope(*x, **how)
+    unread = [t if n == side else torch.full_like(t, float("nan")) for t, n in zip(x, ("q_weight", "k_weight"))]
+    grads = gqa.qk_norm_rope_bwd(to_dev(dz[0]), to_dev(dz[1]), *unread, **how)
+    _sync_ok(gqa)
+    rows = ref.f64(qkv).transpose(0, 2, 1, 3)
+    c, s = _at(cos, sin, pos)
+    for i, (lo, hi, n) in enumerate(((0, Hq, "q_weight"), (Hq, Hq + Hkv, "k_weight"))):
+        want, size = ref.norm_rope(rows[:, lo:hi], w[n], 1e-5, c, s, inter)
+        _near(from_dev(z[i]), want, STEP * np.abs(want) + 2.0 ** -16 * size, n)
+        dx, dw, size, wsize = ref.norm_rope_bwd(ref.f64(dz[i]), rows[:, lo:hi], w[n], 1e-5, c, s, inter)
+        _near(from_dev(grads[i]), dx, STEP * np.abs(dx) + 2.0 ** -16 * size, "gradient under " + n)
+        if n == side:
+            _near(grads[2 + i].cpu().numpy(), dw, 2.0 ** -15 * wsize, "gradient of " + n)
+        else:
+            assert grads[2 + i] is None
+
+
+def test_every_call_on_another_stream(gqa):
+    """The calls on a stream of their own, behind work of the current one, with outputs allocated by them
+    and dropped at once: nothing allocated for a call is given away before the stream has passed it."""
+    torch = torch_mod()
+    N, Hq, Hkv, D, page = 600, 8, 2, 128, 32
+    qkv, w, cos, sin, pos = _rope_inputs((1, N, Hq, Hkv, D, D, False, True, True), 211)
+    how = dict(_dev_weights(w, True), cos=_dev(cos), sin=_dev(sin), positions=_dev(pos[0]))
+    d = to_dev(qkv)[0]
+    q, k, v = d[:, :Hq], d[:, Hq:Hq + Hkv], d[:, Hq + Hkv:]
+    pages = N // page + 2
+    held, new, count, lens = _i32([N]), _i32([1]), _i32([4]), _i32([N])
+    table0 = torch.arange(pages + 4, dtype=torch.int32, device="cuda")[None]
+    side = torch.cuda.Stream()
+
+    def step(stream):
+        pools = [torch.full((pages, page, Hkv, D), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        pools4 = [torch.full((pages, Hkv, page, D // 2 + 4), 0xAB, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        table, free = table0.clone(), torch.arange(pages, pages + 4, dtype=torch.int32, device="cuda")
+        slots = torch.arange(N, dtype=torch.int32, device="cuda")
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        got = []
+        p = gqa.paged_plan(held, new, table, free, count, page_size=page, num_pages=pages + 4, max_tokens=40, stream=stream)
+        z = gqa.qk_norm_rope(q[None].transpose(1, 2), k[None].transpose(1, 2), stream=stream, **how)
+        g = gqa.qk_norm_rope_bwd(*z, q[None].transpose(1, 2), k[None].transpose(1, 2), stream=stream, **how)
+        qa = gqa.qk_norm_rope_append(q, k, v, *pools, slots, stream=stream, **how)
+        gqa.kv4_append(k, v, *pools4, slots, stream=stream)
+        back = gqa.kv4_gather(*pools4, slots, stream=stream)
+        o = gqa.attn_decode_kv4(qa[-1][None], *pools4, lens, table, stream=stream)
+        if stream is not None:
+            torch.cuda.current_stream().wait_stream(stream)
+        for t in (*p, *z, *g, qa, *back, o, *pools, *pools4, table, free):
+            got.append(t.clone())
+        return got
+
+    want = step(None)
+    _sync_ok(gqa)
+    for _ in range(3):
+        got = step(side)
+        noise = [torch.full((1 << 20,), 7.0, device="cuda") for _ in range(4)]  # takes what was given back too early
+        _sync_ok(gqa)
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
+        del noise
