@@ -12,8 +12,9 @@ Around the attention calls, for torch tensors in the same way: ``paged_plan`` (b
 tables and cache rows of a step, on the device), ``qk_norm_rope`` with its backward and
 its cache-writing form, and a paged cache held in 4 bits (``kv4_append``,
 ``kv4_gather``, ``attn_decode_kv4``). Their checks and allocations are in C++
-(``_torch_calls.so``, built with the library), since these calls take microseconds on the
-device. All operands must be on the current device; a ``stream`` other than the current one has to be ordered after it by the caller.
+(``_torch_calls.so``, built with the library where torch with CUDA is installed), since these
+calls take microseconds on the device. All operands must be on the current device; a ``stream``
+other than the current one has to be ordered after it by the caller.
 
 There is no CPU fallback: importing this package fails loudly if the CUDA
 library has not been built.
@@ -792,7 +793,7 @@ def _load_calls():
     _torch()  # before the module, which needs its libraries
     path = os.path.join(_HERE, "_torch_calls.so")
     if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: build the library first "
+        raise ImportError(f"{path} is missing: build the library with torch installed "
                           "(python -c 'import __graft_entry__ as g; g.build()'). There is no fallback.")
     from . import _torch_calls as calls
     calls.set_functions(*[ctypes.cast(getattr(_lib, n), _vp).value for n in (

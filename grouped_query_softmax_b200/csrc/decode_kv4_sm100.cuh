@@ -31,8 +31,9 @@
 // contiguous): no warp waits for another.
 //
 // The bytes are D + 8 a key and KV head; what bounds it is instructions. 64 sequences of 4096 to
-// 32768 keys, 8 KV heads of 4 queries, D = 128: 225 to 255 us, 5.2 to 5.9 TB/s, 79 to 90 % of the
-// measured copy rate, at 449 instructions a 32 keys, 54 % of the issue slots and 55 % of the
+// 32768 keys, 8 KV heads of 4 queries, D = 128: 224 us, 5.9 TB/s, 90 % of the measured copy rate, as long as the
+// SMs run at 1965 MHz; after half a second of such calls the power limit holds them at 1700 MHz and it is
+// 264 us, 5.0 TB/s, 77 %. 449 instructions a 32 keys, 54 % of the issue slots and 55 % of the
 // logic pipe (12 warps an SM; 16 with smaller rings were no faster). 64-key tiles where the
 // scores fit the registers: 32-key tiles took 8 % longer, by what is done once a tile.
 #pragma once
@@ -595,7 +596,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT>::kThreads, Dec4Cfg<D, NT>::kCta
                             e[0] = ex2_approx(e[0]);
                             e[1] = ex2_approx(e[1]);
                             dec4_add2(l[nt], e);
-const float vs = vstep[j][c] * up_step, vss[2] = {vs, vs}, mids[2] = {vmid[j][c], vmid[j][c]};
+                            const float vs = vstep[j][c] * up_step, vss[2] = {vs, vs}, mids[2] = {vmid[j][c], vmid[j][c]};
                             if constexpr (kMasked) {  // such a key's step may be NaN
 #pragma unroll
                                 for (int x = 0; x < 2; ++x) {

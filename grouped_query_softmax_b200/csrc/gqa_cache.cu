@@ -280,7 +280,10 @@ gqa_status check_dec4(int B, int Hq, int Hkv, int Tq, int max_seqlen_k, int D, i
     return GQA_OK;
 }
 
-// N tiles of 8 query rows a CTA takes: as few as hold a group's rows, four at most.
+// N tiles of 8 query rows a CTA takes: as few as hold a group's rows, four at most (more would not fit
+// the registers). us with one / two / four, 18 x 20000 keys, D = 128: 8 rows 48.9 / 67.2 / -, 16 rows 45.9 / 45.9 / 75.9;
+// 64 x 8192 keys of 4 KV heads, D = 64, 16 rows 80.2 / 64.9 / 111. Of 32 rows two passes of two tiles or one of four
+// come out either way: 18 x 20000 keys 44.2 / 51.8, with D = 64 39.4 / 34.3; 16 x 4096 keys of 4 KV heads 37.2 / 34.4.
 int dec4_nt(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 struct Dec4Plan {
@@ -302,7 +305,10 @@ Dec4Plan dec4_plan_for(int B, int Hkv, int rows, int Tq, int max_seqlen_k, int w
     const long long tiles = (long long)B * Hkv * r.n_rc * ((keys + C::kKeys - 1) / C::kKeys);
     r.ctas = (int)std::min<long long>((long long)sm_count() * C::kCtasPerSm, tiles);
     // A cluster a unit, if they all run at once (16 CTAs have to fit a GPC together: half the places)
-    // and have little more to do than the even runs, which pay for their merge with a second launch.
+    // and have little more to do than the even runs, which pay for their merge with a second launch. us with
+    // clusters / runs, 8 KV heads of 4 queries, D = 128: 1 x 4099 keys 7.6 / 13.2, 1 x 32768 19.3 / 24.0, 16 x 4096
+    // 19.9 / 23.6, 16 x 16384 60.4 / 59.4, 1 x 131072 57.7 / 43.9. Where the rounds are about to tip it the rule takes the runs a
+    // little early: one KV head of 32 queries over 32768 keys 31.7 / 34.6.
     const long long units = (long long)B * Hkv * r.n_rc, of_unit = tiles / units;
     const long long places = (long long)sm_count() * C::kCtasPerSm;
     int cluster = 1;

@@ -4,8 +4,9 @@
 // 2i + 1 in its high one, then two bf16 values, the step s and the minimum m. It stands for
 // s * code + m, where m is the row's smallest value (exact: the input is bf16 too),
 // s = bf16((max - min) / 15) and code = round_half_even((x - m) * r), x - m and r = 1 / s each
-// rounded to 32 bits. s is off by at most 2^-9 of itself, so the largest code is round(15 (1 + 2^-9)) = 15
-// and every value is off by at most (1/2 + 15 * 2^-9) s before the bf16 rounding of the read.
+// rounded to 32 bits. s is off by at most 2^-8 of the exact step, so the largest code is
+// round(15 / (1 - 2^-8)) = round(15.06) = 15; the codes are those of s itself, so every value is off by at
+// most (1/2 + 2^-18) s before the bf16 rounding of the read.
 // A row with a NaN or an infinity, or whose max - min exceeds fp32's range, is stored with
 // s = m = NaN: all of it reads as NaN. A step below 2^-126 is stored as 0: the row is m.
 //

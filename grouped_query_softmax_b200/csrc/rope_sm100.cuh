@@ -22,8 +22,9 @@
 // to bf16 at the end is fp32.
 //
 // 4 x 4096 tokens, 32 + 8 heads of 128: forward 57 us, 5.9 TB/s, 90 % of the measured copy rate
-// (77 us with every row summed by itself); backward 97 us, 79 % (16 warps an SM, whose loads do
-// not all overlap). 35197 tokens appended: 148 us, 91 %. 64 tokens appended: 3.5 us, a launch.
+// (77 us with every row summed by itself); backward 98 us, 78 % (16 warps an SM, whose loads do
+// not all overlap; 106 us once the power limit holds the SMs at 1850 of their 1965 MHz). 35197 tokens appended:
+// 148 us, 91 %. 64 tokens appended: 3.5 us, a launch.
 #pragma once
 
 #include "sm100_ptx.cuh"

@@ -524,8 +524,9 @@ GQA_API gqa_status gqa_qk_norm_rope_append(const void* q, const void* k, const v
  * A row of D values is D/2 + 4 bytes: element 2i in the low and 2i + 1 in the high nibble of
  * byte i, then two bf16 values, the step s and the minimum m. It stands for s * code + m, where
  * m is the row's smallest value, s = bf16((max - min) / 15) and code = round_half_even((x - m) *
- * r), x - m and r = 1 / s each rounded to 32 bits: off by at most (1/2 + 15/512) s. A row with a NaN or an
+ * r), x - m and r = 1 / s each rounded to 32 bits: off by at most (1/2 + 2^-18) s. A row with a NaN or an
  * infinity, or whose max - min passes fp32's range, is stored as NaN; a step below 2^-126 as 0.
+ * Steps of 2^113 and more are stored and read back, but gqa_attn_decode_kv4 does not take them.
  * A pool is uint8 [num_pages, Hkv, page_size, D/2 + 4] with free page and head strides.
  */
 typedef struct gqa_kv4_layout {
