@@ -7,9 +7,11 @@
 // the scales stay out of the products, which run on tensor cores in fp16 with fp32 sums. A code
 // needs no conversion: its bits, masked out of the word, are the fp16 subnormal c * 2^-24 (16 c four
 // bits up), so eight codes cost four logic operations and one shift. q is exact in fp16 after a
-// scaling by a power of two a row (see below). w is the only rounding besides the output's; it is
+// scaling by a power of two a row (see below). w is the only operand that is rounded; it is
 // scaled by the largest step seen, since a probability times a step can be of any size, and summed
-// about the middle of the code range (sum_j 8 w_j is one more product). A row's NaN can only reach
+// about the middle of the code range (sum_j 8 w_j is one more product). Over long sequences the fp32 sums'
+// own rounding shows too, since the two differ by little then: 64 sequences of 4096 to 32768 keys are off by 0.0020 of
+// the output where sums in 32 bits of unpacked rows are by 0.0017, both mostly the rounding to bf16; one of 4099 keys by 0.0017. A row's NaN can only reach
 // the queries that see the key: the codes themselves are always finite.
 //
 // Keys are the M dimension of the products and query rows their N (8 a tile), so that one
@@ -32,8 +34,8 @@
 //
 // The bytes are D + 8 a key and KV head; what bounds it is instructions. 64 sequences of 4096 to
 // 32768 keys, 8 KV heads of 4 queries, D = 128: 224 us, 5.9 TB/s, 90 % of the measured copy rate, as long as the
-// SMs run at 1965 MHz; after half a second of such calls the power limit holds them at 1700 MHz and it is
-// 264 us, 5.0 TB/s, 77 %. 449 instructions a 32 keys, 54 % of the issue slots and 55 % of the
+// SMs run at 1965 MHz; after half a second of such calls the power limit holds them near 1700 MHz and it is
+// 264 to 275 us, 4.9 to 5.0 TB/s, 74 to 77 %. 449 instructions a 32 keys, 54 % of the issue slots and 55 % of the
 // logic pipe (12 warps an SM; 16 with smaller rings were no faster). 64-key tiles where the
 // scores fit the registers: 32-key tiles took 8 % longer, by what is done once a tile.
 #pragma once
